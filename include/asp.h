@@ -20,6 +20,11 @@
  *                       stream, the selection for step t+1 on a side stream
  *   asp_quest_*         the page-level comparison path (min/max page metadata)
  *
+ * Around them: K/V append, a cache held in 8 bits (asp_quantize_kv; the scan, the
+ * attention, the append and the decode step take it in place of a bf16 cache), and a
+ * cache held to a budget (asp_attend_accumulate sums the attention each cached token
+ * gets, asp_evict_kv keeps the tokens with the largest sums).
+ *
  * Conventions for every call:
  *   - Pointers named as device memory must be device memory of the current CUDA
  *     device; they stay owned by the caller.  The library never allocates device
@@ -70,7 +75,10 @@ typedef enum {
   ASP_ERR_DEVICE = 6        /* asp_device_status: a kernel recorded a device-side fault */
 } asp_status;
 
-typedef enum { ASP_F32 = 0, ASP_BF16 = 1 } asp_dtype;
+/* ASP_E4M3 and ASP_I8 are cache types only (see asp_kv): a value is code * scale with
+ * one fp32 scale per block of tokens, KV head and side (K or V).  E4M3 codes are 8-bit
+ * floats (largest 448), I8 codes integers in [-127, 127]. */
+typedef enum { ASP_F32 = 0, ASP_BF16 = 1, ASP_E4M3 = 2, ASP_I8 = 3 } asp_dtype;
 
 /* How the ridge coefficients of one window become weights (softmax is the
  * method's softmax normalisation; RAW keeps the coefficients). */
@@ -92,6 +100,7 @@ typedef enum { ASP_POOL_PREDICTIONS = 0, ASP_POOL_FEATURES = 1 } asp_pool_mode;
 #define ASP_DEV_TAIL_LIMIT 0x8   /* a tail longer than max_tail was truncated */
 #define ASP_DEV_SELECT     0x10  /* a selection output position past C was skipped (a first-digit
                                     histogram that does not match the scores) */
+#define ASP_DEV_NONFINITE  0x40  /* an infinity or NaN was written to an 8-bit cache (see asp_quantize_kv) */
 #define ASP_DEV_NAN_SCORE  0x20  /* the selection read a NaN score: invalid input, the chosen set
                                     is then unspecified (it never holds more than C tokens) */
 
@@ -103,13 +112,23 @@ typedef enum { ASP_POOL_PREDICTIONS = 0, ASP_POOL_FEATURES = 1 } asp_pool_mode;
  * seq_lens[b] = T_b, the number of valid tokens of sequence b (device int32 [batch],
  * 0 <= T_b <= t_max; larger values are clamped to t_max).  NULL means T_b = t_max.
  * Paged caches require seq_lens and page_table (device int32 [batch, max_pages]),
- * t_max <= max_pages * page_size.  k, v must be 16-byte aligned. */
+ * t_max <= max_pages * page_size.  k, v must be 16-byte aligned.
+ *
+ * 8-bit caches (kv_dtype ASP_E4M3 or ASP_I8): k, v hold one byte per value, laid out as
+ * above, and every scale_block consecutive tokens of a KV head share a scale:
+ *   page_size == 0: k_scale, v_scale are [batch, n_kv_heads, ceil(t_max / scale_block)];
+ *   page_size  > 0: [n_pages, n_kv_heads, page_size / scale_block] (a block lies within a
+ *                   page: scale_block must divide page_size).
+ * Scales are read as they are (any positive normal fp32; precision holds for scales of at
+ * least 2^-100); those the library writes are powers of two.  The calls that take an
+ * 8-bit cache say so; the others return ASP_ERR_UNSUPPORTED for it.  The last four
+ * fields are read for 8-bit caches only. */
 typedef struct {
   int batch;
   int n_kv_heads;
   int head_dim;          /* 64 or 128 */
   int t_max;             /* token capacity of a sequence; row stride of score buffers */
-  asp_dtype kv_dtype;    /* ASP_F32 or ASP_BF16 */
+  asp_dtype kv_dtype;    /* ASP_F32, ASP_BF16, ASP_E4M3 or ASP_I8 */
   const void* k;
   const void* v;
   int page_size;
@@ -117,6 +136,10 @@ typedef struct {
   int max_pages;
   int n_pages;           /* physical pages in the pool (paged only) */
   const int32_t* seq_lens;
+  float* k_scale;        /* 8-bit caches: device fp32, laid out as described above */
+  float* v_scale;
+  int scale_block;       /* tokens that share a scale: 16, 32, 64 or 128 */
+  asp_dtype src_dtype;   /* type of the rows appended to an 8-bit cache: ASP_F32 or ASP_BF16 */
 } asp_kv;
 
 /* Predictor configuration (host memory). */
@@ -162,7 +185,9 @@ ASP_API asp_status asp_predict_query(float* qhist, int ring_start, const void* q
  * filtering); research-map summary, "Key results" (Qwen3 GQA models).
  * scores[b, h, j] = max over the G query heads g of KV head h of
  *                   (qpred[b, h*G + g, :] . k[b, h, j, :]) / sqrt(head_dim),  j < T_b.
- * Entries j >= T_b of a row are not written.  fp32 arithmetic.
+ * Entries j >= T_b of a row are not written.  fp32 arithmetic.  8-bit caches: k is
+ * code * scale; every product of a code with the query (two fp16 parts: 22 bits of each
+ * head's largest channel) is exact in the fp32 sum, which the scale then multiplies.
  * qpred  : device fp32 [batch, n_q_heads, head_dim].
  * scores : device fp32 [batch, n_kv_heads, t_max], written.
  * Errors: ASP_ERR_INVALID_ARG; ASP_ERR_UNSUPPORTED (G not in {1,2,4,8}, head_dim
@@ -172,7 +197,7 @@ ASP_API asp_status asp_score_keys(const float* qpred, int n_q_heads, const asp_k
 
 /* Step 2 on the CUDA cores whatever the key type: the scan asp_score_keys runs for
  * fp32 keys and page sizes other than 16, and for bf16 keys the comparison of its
- * tensor-core scan (same arguments, errors and results within the score tolerance;
+ * tensor-core scan; not for 8-bit caches (same arguments, errors and results within the score tolerance;
  * the tensor-core path replaced it for bf16 keys because it reaches the copy
  * bandwidth where this one is bound by instruction issue). */
 ASP_API asp_status asp_score_keys_cuda_cores(const float* qpred, int n_q_heads, const asp_kv* kv, float* scores,
@@ -212,9 +237,16 @@ ASP_API asp_status asp_select_topk(const float* scores, const int32_t* seq_lens,
  * tail_begin : device int32 [batch] or NULL (no tail); max_tail bounds T_b - tail_begin
  *              (longer tails are truncated and flagged).  max_tail = t_max with
  *              tail_begin = 0 and count = 0 gives dense attention.
- * out        : device [batch, n_q_heads, head_dim] in kv_dtype, written.
+ * out        : device [batch, n_q_heads, head_dim] in kv_dtype, written; in q_dtype for an
+ *              8-bit cache.
  * lse        : device fp32 [batch, n_q_heads] or NULL.
- * workspace  : device scratch of at least asp_attend_workspace_bytes(...) bytes,
+ * 8-bit caches: rows are read as codes and enter fp16 matrix products exactly; the scales
+ * multiply the fp32 logits and softmax weights.  The weights are rounded to fp16 for a
+ * bf16 query (2^-11 relative, below the output's own rounding of 2^-8) and split into two
+ * fp16 parts for an fp32 query; with V's scale, a weight below 2^-28 of a head's largest
+ * keeps fewer bits (its error stays below 2^-38 of the largest).
+ * workspace  : device scratch of at least asp_attend_workspace_bytes(...) bytes (for an
+ *              8-bit cache asp_attend_workspace_bytes_kv(...)),
  *              16-byte aligned; contents need no initialisation.  May be NULL when
  *              asp_attend_workspace_bytes(...) is 0.
  * Errors: ASP_ERR_INVALID_ARG; ASP_ERR_UNSUPPORTED; ASP_ERR_WORKSPACE. */
@@ -234,6 +266,11 @@ ASP_API size_t asp_attend_workspace_bytes(int batch, int n_q_heads, int n_kv_hea
  * of its arguments, 0 for invalid sizes. */
 ASP_API size_t asp_decode_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int head_dim, int C,
                                           int max_tail);
+
+/* The same two for a given cache, whatever its type (k, v, tables and scales are not
+ * looked at and may be NULL); 0 for invalid arguments. */
+ASP_API size_t asp_attend_workspace_bytes_kv(const asp_kv* kv, int n_q_heads, int C, int max_tail);
+ASP_API size_t asp_decode_workspace_bytes_kv(const asp_kv* kv, int n_q_heads, int C, int max_tail);
 
 /* Bytes of one predictor-factor buffer of asp_decode_step (pred_factor_cur / _next):
  * per query head the scaled rows of the lag Gram's Cholesky factor and its inverse
@@ -268,7 +305,8 @@ ASP_API asp_status asp_sparse_attend_noalloc(const void* q, asp_dtype q_dtype, i
  * The new token's K and V appended to the cache (the cache management that
  * surrounds the steps; reproduction card, "Key finding", and abstract,
  * component (2): the cache side keeps the KV cache current while decoding).
- * k_new, v_new : device [batch, n_kv_heads, head_dim] in kv_dtype, 16-byte aligned.
+ * k_new, v_new : device [batch, n_kv_heads, head_dim] in kv_dtype (in kv->src_dtype for an
+ *              8-bit cache), 16-byte aligned.
  * For every sequence b the token goes to position T = seq_lens[b] (contiguous:
  * row T of [b, h]; paged: row T % page_size of page page_table[b][T / page_size],
  * which the caller has allocated), then tail_begin_out[b] = T (when not NULL: the
@@ -279,9 +317,92 @@ ASP_API asp_status asp_sparse_attend_noalloc(const void* q, asp_dtype q_dtype, i
  *              sets the page's bounds, later tokens widen them.
  * A sequence at capacity (T == t_max, or past its pages) or whose page is not
  * valid is left unchanged and ASP_DEV_BAD_PAGE is recorded (asp_device_status).
+ * 8-bit caches: a token that opens a scale block sets the block's scale as in
+ * asp_quantize_kv; a later token whose values do not fit raises it to the power of two
+ * that they need and the block's older codes are re-rounded at the new scale (for E4M3
+ * this is exact but for values that become subnormal; for I8 the roundings add up to less
+ * than one step of the final scale, since every raise at least doubles it).
+ * quest_meta must be NULL for 8-bit caches (ASP_ERR_UNSUPPORTED).
  * Asynchronous on `stream`. */
 ASP_API asp_status asp_append_kv(const asp_kv* kv, const void* k_new, const void* v_new, int32_t* tail_begin_out,
                                  void* quest_meta, int quest_page, asp_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The 8-bit cache: filled from wide rows and read back (kv_dtype ASP_E4M3 or ASP_I8).
+ * Blocks of scale_block tokens share, per KV head and side, the scale
+ *   s = the smallest power of two >= 2^-100 with max |x| <= qmax * s   (qmax 448 or 127)
+ * over the finite values of the block's tokens; a code is x / s (exact) rounded to the
+ * nearest code, ties to even: for E4M3 an error of at most 2^-4 relative (half a step of
+ * 3 fraction bits; 2^-10 s below 2^-6 s), for I8 at most s / 2.  Infinities become the
+ * largest code, NaN the E4M3 NaN or the I8 zero, and either sets ASP_DEV_NONFINITE.
+ *
+ * asp_quantize_kv writes tokens [0, T_b) of every sequence from k_src, v_src (both
+ * [batch, n_kv_heads, >= T_b tokens, head_dim] of src_dtype with the given element strides
+ * for batch, head and token; channels contiguous; rows 16-byte aligned: base addresses and
+ * strides multiples of 16 bytes) and the scales of the blocks that hold them.  Codes of
+ * tokens >= T_b and scales of blocks past them are left as they were.  An invalid page is
+ * skipped and flagged (ASP_DEV_BAD_PAGE).
+ * asp_dequantize_kv writes code * scale of the same tokens to k_dst, v_dst of dst_dtype
+ * (laid out by strides in the same way), rounded to nearest; other tokens are not written.
+ * Errors: ASP_ERR_INVALID_ARG (null, misaligned, bad types or negative strides);
+ * ASP_ERR_UNSUPPORTED (a cache that is not 8-bit, head_dim not 64/128, scale_block not one
+ * of 16, 32, 64, 128 or not dividing page_size). */
+ASP_API asp_status asp_quantize_kv(const asp_kv* kv, const void* k_src, const void* v_src, asp_dtype src_dtype,
+                                   int64_t stride_batch, int64_t stride_head, int64_t stride_token,
+                                   asp_stream_t stream);
+ASP_API asp_status asp_dequantize_kv(const asp_kv* kv, void* k_dst, void* v_dst, asp_dtype dst_dtype,
+                                     int64_t stride_batch, int64_t stride_head, int64_t stride_token,
+                                     asp_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention that also sums the weight each cached token gets (every cache type).
+ * out and lse as asp_sparse_attend over the same S, and for every token j of S
+ *   acc[b, h, j] += sum over the G query heads g of KV head h of
+ *                   exp(q[b, h*G+g] . k_j / sqrt(d) - lse[b, h*G+g]);
+ * entries of tokens outside S are left as they were.  Sums are fp32.  Selected indices
+ * must be distinct (each row's weight is added once per listing, in no fixed order).
+ * acc        : device fp32 [batch, n_kv_heads, t_max].
+ * workspace  : asp_accumulate_workspace_bytes(...) bytes, 256-byte aligned, no
+ *              initialisation needed; it holds the logits between the passes.  Two calls
+ *              that may overlap (streams, captured graphs) need workspaces of their own.
+ * Other arguments and errors as asp_sparse_attend. */
+ASP_API asp_status asp_attend_accumulate(const void* q, asp_dtype q_dtype, int n_q_heads, const asp_kv* kv,
+                                         const int32_t* idx, const int32_t* count, int C, const int32_t* tail_begin,
+                                         int max_tail, void* out, float* lse, float* acc, void* workspace,
+                                         size_t workspace_bytes, asp_stream_t stream);
+
+/* Bytes of workspace for these arguments (a pure function of them; k, v, tables and
+ * scales are not looked at); 0 for invalid arguments. */
+ASP_API size_t asp_accumulate_workspace_bytes(const asp_kv* kv, int n_q_heads, int C, int max_tail);
+
+/* ---------------------------------------------------------------------------
+ * Eviction to a budget of C tokens by accumulated attention (every cache type).
+ * A sequence with T_b <= C keeps all its tokens and nothing of it moves.  Otherwise every
+ * KV head keeps its first n_sink tokens, its last n_recent tokens and, of the rest, those
+ * with the largest acc[b, h, j] (ties to the lowest index) up to C in all, and its kept
+ * tokens move, in order, to positions 0 .. C - 1 of the cache, in place:
+ *   idx[b, h, i] = the old position of the token now at i, ascending, -1 past count;
+ *   count[b, h]  = min(C, T_b); seq_lens[b] = min(C, T_b), written on the device;
+ *   acc_out[b, h, i] = acc[b, h, idx[b, h, i]] for i < count, 0 from there to t_max.
+ * 8-bit caches: the moved rows form new scale blocks; codes are rounded again at the
+ * scale asp_quantize_kv would choose for the kept values.  Rows past count, and pages past
+ * them, are left as they were (the caller may free those pages).  Selections and page
+ * bounds made before the call refer to old positions and have to be made again.  Pages
+ * must not be shared between sequences.  kv->seq_lens must not be NULL.
+ * acc        : device fp32 [batch, n_kv_heads, t_max], finite (a NaN sets
+ *              ASP_DEV_NAN_SCORE, the kept set is then unspecified).
+ * acc_out    : the same shape: acc itself or a buffer apart from it.
+ * idx, count : device int32 [batch, n_kv_heads, C] and [batch, n_kv_heads], written.
+ * workspace  : asp_evict_workspace_bytes(...) bytes, 256-byte aligned, no initialisation
+ *              needed.
+ * An invalid page is skipped (its rows are neither read nor written, a kept token of one
+ * counts as zero) and flagged (ASP_DEV_BAD_PAGE).
+ * Errors: ASP_ERR_INVALID_ARG (null pointers, C < 1, n_sink or n_recent negative or
+ * n_sink + n_recent > C); ASP_ERR_UNSUPPORTED; ASP_ERR_WORKSPACE. */
+ASP_API asp_status asp_evict_kv(const asp_kv* kv, const float* acc, float* acc_out, int C, int n_sink, int n_recent,
+                                int32_t* idx, int32_t* count, void* workspace, size_t workspace_bytes,
+                                asp_stream_t stream);
+ASP_API size_t asp_evict_workspace_bytes(const asp_kv* kv, int C);
 
 /* ---------------------------------------------------------------------------
  * One asynchronous decode step (steps 1-4).
@@ -300,7 +421,9 @@ ASP_API asp_status asp_append_kv(const asp_kv* kv, const void* k_new, const void
  * ev_sel_done completes.  While s_main is being captured (CUDA graphs) the step
  * leaves out its wait for ev_sel_done: the caller then orders the graph launches on
  * one stream, and ends each capture with s_main waiting for ev_sel_done, so that
- * the graph joins both streams.  workspace: at least asp_decode_workspace_bytes(...)
+ * the graph joins both streams.  An 8-bit cache is taken like a bf16 one (out is then in
+ * q_dtype, k_new and v_new in kv->src_dtype, quest_meta NULL).  workspace: at least
+ * asp_decode_workspace_bytes(...) (8-bit caches: asp_decode_workspace_bytes_kv(...))
  * bytes, 256-byte aligned, no initialisation needed (ASP_ERR_WORKSPACE otherwise).  timing: NULL, or 8 events recorded around the kernels
  * (begin/end of predict, score, select on s_side; attend on s_main) for profiling. */
 typedef struct {

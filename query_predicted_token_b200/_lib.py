@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_float, c_int, c_int32, c_long, c_size_t, c_void_p
+from ctypes import POINTER, c_float, c_int, c_int32, c_int64, c_long, c_size_t, c_void_p
 from typing import Optional, Sequence
 
 import torch
@@ -17,17 +17,19 @@ import torch
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libasp.so")
 
 ASP_OK, ASP_ERR_INVALID_ARG, ASP_ERR_UNSUPPORTED, ASP_ERR_WORKSPACE, ASP_ERR_CUDA, ASP_ERR_TIMEOUT, ASP_ERR_DEVICE = range(7)
-ASP_F32, ASP_BF16 = 0, 1
+ASP_F32, ASP_BF16, ASP_E4M3, ASP_I8 = 0, 1, 2, 3
 ASP_COEF_SOFTMAX, ASP_COEF_RAW = 0, 1
 ASP_POOL_PREDICTIONS, ASP_POOL_FEATURES = 0, 1
 ASP_DEV_BAD_INDEX, ASP_DEV_BAD_PAGE, ASP_DEV_WAIT_LIMIT, ASP_DEV_TAIL_LIMIT, ASP_DEV_SELECT = 1, 2, 4, 8, 16
 ASP_DEV_NAN_SCORE = 32
+ASP_DEV_NONFINITE = 64
 
 # every entry point of include/asp.h with its ctypes signature
 class AspKv(ctypes.Structure):
     _fields_ = [("batch", c_int), ("n_kv_heads", c_int), ("head_dim", c_int), ("t_max", c_int),
                 ("kv_dtype", c_int), ("k", c_void_p), ("v", c_void_p), ("page_size", c_int),
-                ("page_table", c_void_p), ("max_pages", c_int), ("n_pages", c_int), ("seq_lens", c_void_p)]
+                ("page_table", c_void_p), ("max_pages", c_int), ("n_pages", c_int), ("seq_lens", c_void_p),
+                ("k_scale", c_void_p), ("v_scale", c_void_p), ("scale_block", c_int), ("src_dtype", c_int)]
 
 
 class AspPredCfg(ctypes.Structure):
@@ -56,6 +58,16 @@ SIGNATURES = {
                                   c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "asp_attend_workspace_bytes": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int]),
     "asp_decode_workspace_bytes": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int]),
+    "asp_attend_workspace_bytes_kv": (c_size_t, [POINTER(AspKv), c_int, c_int, c_int]),
+    "asp_decode_workspace_bytes_kv": (c_size_t, [POINTER(AspKv), c_int, c_int, c_int]),
+    "asp_attend_accumulate": (c_int, [c_void_p, c_int, c_int, POINTER(AspKv), c_void_p, c_void_p, c_int, c_void_p,
+                                      c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "asp_accumulate_workspace_bytes": (c_size_t, [POINTER(AspKv), c_int, c_int, c_int]),
+    "asp_evict_kv": (c_int, [POINTER(AspKv), c_void_p, c_void_p, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p,
+                             c_size_t, c_void_p]),
+    "asp_evict_workspace_bytes": (c_size_t, [POINTER(AspKv), c_int]),
+    "asp_quantize_kv": (c_int, [POINTER(AspKv), c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p]),
+    "asp_dequantize_kv": (c_int, [POINTER(AspKv), c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p]),
     "asp_pred_factor_bytes": (c_size_t, [c_int, c_int, POINTER(AspPredCfg)]),
     "asp_sparse_attend_noalloc": (c_int, [c_void_p, c_int, c_int, POINTER(AspKv), c_void_p, c_void_p, c_int, c_void_p,
                                           c_int, c_void_p, c_void_p, c_void_p]),
@@ -131,17 +143,52 @@ def dtype_code(t: torch.Tensor) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
+_CACHE_8 = {torch.float8_e4m3fn: ASP_E4M3, torch.int8: ASP_I8}
+
+
+def scale_shape(k: torch.Tensor, scale_block: int, paged: bool) -> tuple:
+    """Shape of the scales of an 8-bit cache side: ``[B, Hkv, ceil(T / scale_block)]``, or
+    ``[n_pages, Hkv, P / scale_block]`` for pages."""
+    rows = k.shape[2]
+    if paged and rows % scale_block:
+        raise ValueError(f"scale_block {scale_block} does not divide the page size {rows}")
+    return (k.shape[0], k.shape[1], -(-rows // scale_block))
+
+
 class KV:
     """A KV cache described for the C ABI (holds references to its tensors).
 
     Contiguous: ``k, v [B, Hkv, T, d]``.  Paged: ``k, v [n_pages, Hkv, P, d]`` with
     ``page_table [B, max_pages]`` int32 and ``seq_lens [B]`` int32.
+
+    8-bit caches: ``k, v`` of ``torch.float8_e4m3fn`` or ``torch.int8`` with fp32
+    ``k_scale, v_scale`` (:func:`scale_shape`), one scale per ``scale_block`` tokens (16,
+    32, 64 or 128); ``src_dtype`` is the type of the rows :func:`append_kv` takes.
     """
 
     def __init__(self, k: torch.Tensor, v: Optional[torch.Tensor], seq_lens: Optional[torch.Tensor] = None,
-                 page_table: Optional[torch.Tensor] = None, t_max: Optional[int] = None, batch: Optional[int] = None):
+                 page_table: Optional[torch.Tensor] = None, t_max: Optional[int] = None, batch: Optional[int] = None,
+                 k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                 scale_block: int = 0, src_dtype: torch.dtype = torch.bfloat16):
         self.k, self.v, self.seq_lens, self.page_table = k, v, seq_lens, page_table
+        self.k_scale, self.v_scale = k_scale, v_scale
         d = k.shape[-1]
+        code = _CACHE_8.get(k.dtype)
+        if code is None:
+            code, k_scale, v_scale, scale_block = dtype_code(k), None, None, 0
+        else:
+            if scale_block not in (16, 32, 64, 128):
+                raise ValueError(f"scale_block {scale_block}: 16, 32, 64 or 128 tokens share a scale")
+            if v is not None and v.dtype != k.dtype:
+                raise TypeError(f"k is {k.dtype}, v is {v.dtype}")
+            if page_table is None and t_max is not None and t_max != k.shape[2]:
+                raise ValueError(f"t_max {t_max}: a contiguous 8-bit cache holds {k.shape[2]} tokens per row")
+            want = scale_shape(k, scale_block, page_table is not None)
+            for name, x, s in (("k_scale", k, k_scale), ("v_scale", v, v_scale)):
+                if x is None:
+                    continue
+                if s is None or s.dtype != torch.float32 or tuple(s.shape) != want or not s.is_contiguous():
+                    raise ValueError(f"{name}: a contiguous fp32 tensor of shape {want} is needed")
         if page_table is None:
             B, Hkv, T, _ = k.shape
             page_size, max_pages, n_pages = 0, 0, 0
@@ -150,9 +197,10 @@ class KV:
             n_pages, Hkv, page_size, _ = k.shape
             B, max_pages = page_table.shape
             t_max = max_pages * page_size if t_max is None else t_max
-        self.struct = AspKv(int(B if batch is None else batch), int(Hkv), int(d), int(t_max), dtype_code(k),
+        self.struct = AspKv(int(B if batch is None else batch), int(Hkv), int(d), int(t_max), code,
                             _ptr(k), _ptr(v), int(page_size), _ptr(page_table), int(max_pages), int(n_pages),
-                            _ptr(seq_lens))
+                            _ptr(seq_lens), _ptr(k_scale), _ptr(v_scale), int(scale_block),
+                            ASP_F32 if src_dtype == torch.float32 else ASP_BF16)
         self.batch, self.n_kv_heads, self.head_dim, self.t_max = int(B), int(Hkv), int(d), int(t_max)
         self.page_size = int(page_size)
 
@@ -210,6 +258,19 @@ def attend_workspace_bytes(batch: int, n_q_heads: int, n_kv_heads: int, head_dim
     return int(lib().asp_attend_workspace_bytes(batch, n_q_heads, n_kv_heads, head_dim, int(C), int(max_tail)))
 
 
+def attend_workspace_bytes_kv(kv: KV, n_q_heads: int, C: int, max_tail: int = 0) -> int:
+    """Workspace of :func:`sparse_attend` for this cache, 8-bit ones included."""
+    return int(lib().asp_attend_workspace_bytes_kv(kv.ref, int(n_q_heads), int(C), int(max_tail)))
+
+
+def accumulate_workspace_bytes(kv: KV, n_q_heads: int, C: int, max_tail: int = 0) -> int:
+    return int(lib().asp_accumulate_workspace_bytes(kv.ref, int(n_q_heads), int(C), int(max_tail)))
+
+
+def evict_workspace_bytes(kv: KV, C: int) -> int:
+    return int(lib().asp_evict_workspace_bytes(kv.ref, int(C)))
+
+
 def sparse_attend(q: torch.Tensor, kv: KV, idx: Optional[torch.Tensor], count: Optional[torch.Tensor], C: int,
                   out: torch.Tensor, lse: Optional[torch.Tensor] = None, tail_begin: Optional[torch.Tensor] = None,
                   max_tail: int = 0, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -228,6 +289,55 @@ def sparse_attend_noalloc(q: torch.Tensor, kv: KV, idx: Optional[torch.Tensor], 
     _check("asp_sparse_attend_noalloc", lib().asp_sparse_attend_noalloc(
         _ptr(q), dtype_code(q), q.shape[1], kv.ref, _ptr(idx), _ptr(count), int(C), _ptr(tail_begin),
         int(max_tail), _ptr(out), _ptr(lse), _stream(stream)))
+
+
+def attend_accumulate(q: torch.Tensor, kv: KV, idx: Optional[torch.Tensor], count: Optional[torch.Tensor], C: int,
+                      out: torch.Tensor, acc: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                      tail_begin: Optional[torch.Tensor] = None, max_tail: int = 0,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """:func:`sparse_attend` that also adds to ``acc [B, Hkv, t_max]`` (fp32) the softmax
+    weight each attended token gets, summed over the query heads of its KV head."""
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("asp_attend_accumulate", lib().asp_attend_accumulate(
+        _ptr(q), dtype_code(q), q.shape[1], kv.ref, _ptr(idx), _ptr(count), int(C), _ptr(tail_begin), int(max_tail),
+        _ptr(out), _ptr(lse), _ptr(acc), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def evict_kv(kv: KV, acc: torch.Tensor, C: int, idx: torch.Tensor, count: torch.Tensor, n_sink: int = 0,
+             n_recent: int = 0, acc_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+             stream=None) -> None:
+    """Keeps C tokens per (sequence, KV head): the first ``n_sink``, the last ``n_recent``
+    and of the rest those with the largest ``acc``; they move to the front of the cache, in
+    order, and ``kv.seq_lens`` shrinks on the device.  ``idx, count`` get the old positions,
+    ``acc_out`` (``acc`` itself if None) the sums of the kept tokens."""
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("asp_evict_kv", lib().asp_evict_kv(kv.ref, _ptr(acc), _ptr(acc if acc_out is None else acc_out), int(C),
+                                              int(n_sink), int(n_recent), _ptr(idx), _ptr(count), _ptr(workspace),
+                                              ws_bytes, _stream(stream)))
+
+
+def _rows8(fn: str, kv: KV, k: torch.Tensor, v: torch.Tensor):
+    for name, x in (("k", k), ("v", v)):
+        if x.dim() != 4 or x.shape[0] != kv.batch or x.shape[1] != kv.n_kv_heads or x.shape[3] != kv.head_dim or \
+                x.stride(3) != 1:
+            raise ValueError(f"{fn}: {name} must be [{kv.batch}, {kv.n_kv_heads}, tokens, {kv.head_dim}] with "
+                             f"contiguous channels")
+    if k.dtype != v.dtype or k.stride() != v.stride():
+        raise ValueError(f"{fn}: k and v must have the same type and strides")
+    return dtype_code(k), k.stride(0), k.stride(1), k.stride(2)
+
+
+def quantize_kv(kv: KV, k_src: torch.Tensor, v_src: torch.Tensor, stream=None) -> None:
+    """Fills an 8-bit cache's tokens [0, seq_lens) from ``k_src, v_src [B, Hkv, tokens, d]``
+    (bf16 or fp32; any strides with contiguous channels, the same for both)."""
+    _check("asp_quantize_kv", lib().asp_quantize_kv(kv.ref, _ptr(k_src), _ptr(v_src),
+                                                    *_rows8("quantize_kv", kv, k_src, v_src), _stream(stream)))
+
+
+def dequantize_kv(kv: KV, k_dst: torch.Tensor, v_dst: torch.Tensor, stream=None) -> None:
+    """The values of an 8-bit cache's tokens [0, seq_lens) into ``k_dst, v_dst``."""
+    _check("asp_dequantize_kv", lib().asp_dequantize_kv(kv.ref, _ptr(k_dst), _ptr(v_dst),
+                                                        *_rows8("dequantize_kv", kv, k_dst, v_dst), _stream(stream)))
 
 
 def quest_build_meta(kv: KV, quest_page: int, meta: torch.Tensor, stream=None) -> None:
@@ -314,7 +424,7 @@ class DecodeState:
         self.idx = [torch.full((B, Hkv, C), -1, dtype=torch.int32, device=dev) for _ in range(2)]
         self.count = [torch.zeros(B, Hkv, dtype=torch.int32, device=dev) for _ in range(2)]
         self.cur = 0
-        ws = int(lib().asp_decode_workspace_bytes(B, n_q_heads, Hkv, d, C, max_tail if tail_begin is not None else 0))
+        ws = int(lib().asp_decode_workspace_bytes_kv(kv.ref, n_q_heads, C, max_tail if tail_begin is not None else 0))
         self.workspace = torch.empty(max(ws, 16), dtype=torch.uint8, device=dev)
         fb = int(lib().asp_pred_factor_bytes(B, n_q_heads, ctypes.byref(cfg.struct))) if precompute_factor else 0
         self.pred_factor = [torch.empty(fb // 8, dtype=torch.float64, device=dev) for _ in range(2)] if fb else None

@@ -70,11 +70,15 @@ bool group_ok(int n_q_heads, int n_kv) {
   return g == 1 || g == 2 || g == 4 || g == 8;
 }
 
-// Validates a KV description; need_v: the call reads v too.
-asp_status check_kv(const asp_kv* kv, bool need_v) {
+bool is8(const asp_kv* kv) { return kv->kv_dtype == ASP_E4M3 || kv->kv_dtype == ASP_I8; }
+bool is_wide(asp_dtype t) { return t == ASP_F32 || t == ASP_BF16; }
+
+// Validates a KV description; need_v: the call reads v too; take8: it takes 8-bit caches.
+asp_status check_kv(const asp_kv* kv, bool need_v, bool take8 = false) {
   if (!kv) return ASP_ERR_INVALID_ARG;
   if (kv->batch <= 0 || kv->n_kv_heads <= 0 || kv->t_max <= 0) return ASP_ERR_INVALID_ARG;
-  if (kv->kv_dtype != ASP_F32 && kv->kv_dtype != ASP_BF16) return ASP_ERR_INVALID_ARG;
+  if (!is_wide(kv->kv_dtype) && !is8(kv)) return ASP_ERR_INVALID_ARG;
+  if (is8(kv) && !take8) return ASP_ERR_UNSUPPORTED;
   if (kv->head_dim != 64 && kv->head_dim != 128) return ASP_ERR_UNSUPPORTED;
   if (!kv->k || (need_v && !kv->v)) return ASP_ERR_INVALID_ARG;
   if (!aligned16(kv->k) || (need_v && !aligned16(kv->v))) return ASP_ERR_INVALID_ARG;
@@ -85,6 +89,14 @@ asp_status check_kv(const asp_kv* kv, bool need_v) {
     if (!kv->page_table || !kv->seq_lens || kv->max_pages <= 0 || kv->n_pages <= 0) return ASP_ERR_INVALID_ARG;
     if ((long)kv->max_pages * kv->page_size < kv->t_max) return ASP_ERR_INVALID_ARG;
   }
+  if (is8(kv)) {
+    const int bl = kv->scale_block;
+    if (bl != 16 && bl != 32 && bl != 64 && bl != 128) return ASP_ERR_UNSUPPORTED;
+    if (kv->page_size > 0 && kv->page_size % bl) return ASP_ERR_UNSUPPORTED;
+    if (!kv->k_scale || (need_v && !kv->v_scale)) return ASP_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(kv->k_scale) & 3u) || (reinterpret_cast<uintptr_t>(kv->v_scale) & 3u))
+      return ASP_ERR_INVALID_ARG;
+  }
   return ASP_OK;
 }
 
@@ -93,6 +105,16 @@ KvView view_of(const asp_kv* kv) {
   v.k = kv->k;
   v.v = kv->v;
   v.kv_f32 = kv->kv_dtype == ASP_F32;
+  v.kv8 = kv->kv_dtype == ASP_E4M3 ? 1 : (kv->kv_dtype == ASP_I8 ? 2 : 0);
+  v.k_scale = v.v_scale = nullptr;
+  v.block_shift = v.blocks_per_row = 0;
+  if (v.kv8) {
+    v.k_scale = kv->k_scale;
+    v.v_scale = kv->v_scale;
+    while ((1 << v.block_shift) < kv->scale_block) ++v.block_shift;
+    v.blocks_per_row = kv->page_size ? kv->page_size / kv->scale_block
+                                     : (int)(((long)kv->t_max + kv->scale_block - 1) / kv->scale_block);
+  }
   v.batch = kv->batch;
   v.n_kv = kv->n_kv_heads;
   v.head_dim = kv->head_dim;
@@ -133,6 +155,37 @@ size_t decode_hist_offset(int batch, int n_q_heads, int n_kv_heads, int head_dim
   return ((att + 255) / 256) * 256;
 }
 
+// What sets the attention's plan: sizes and cache type.
+asp::FlatPlan flat_plan_of(const asp_kv* kv, int n_q_heads, int C, int mt, bool accumulate, int ctas_per_sm) {
+  return asp::flat_plan(kv->batch, n_q_heads, kv->n_kv_heads, kv->head_dim, C, mt, is8(kv), accumulate, ctas_per_sm);
+}
+
+// Sizes a workspace is asked for (no pointers are looked at).
+bool sizes_ok(const asp_kv* kv, int n_q_heads, int C, int max_tail) {
+  return kv && kv->batch > 0 && kv->n_kv_heads > 0 && (long)kv->batch * kv->n_kv_heads <= kMaxGridY &&
+         (kv->head_dim == 64 || kv->head_dim == 128) && (is_wide(kv->kv_dtype) || is8(kv)) &&
+         group_ok(n_q_heads, kv->n_kv_heads) && C >= 0 && max_tail >= 0 && (long)C + max_tail >= 1 &&
+         (long)C + max_tail <= (1L << 30);
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Workspace of asp_attend_accumulate for an fp32 cache: the attention's partials, the lse,
+// the logits.
+struct WideAccumulate {
+  size_t lse_off, logits_off, bytes;
+  int row_stride;
+};
+WideAccumulate wide_accumulate(const asp_kv* kv, int n_q_heads, int C, int mt, size_t partials) {
+  WideAccumulate w;
+  const size_t heads = (size_t)kv->batch * n_q_heads;
+  w.row_stride = (int)(((long)C + mt + 15) / 16 * 16);
+  w.lse_off = round256(partials);
+  w.logits_off = w.lse_off + round256(heads * 4);
+  w.bytes = w.logits_off + round256(heads * w.row_stride * 4);
+  return w;
+}
+
 asp::PredictArgs predict_args(float* qhist, int ring_start, const void* q_new, asp_dtype q_new_dtype, int batch,
                               int n_q_heads, int head_dim, const asp_pred_cfg* cfg, float* qpred) {
   asp::PredictArgs a;
@@ -164,8 +217,9 @@ asp::PredictArgs predict_args(float* qhist, int ring_start, const void* q_new, a
 
 asp_status check_attend(const void* q, asp_dtype q_dtype, int n_q_heads, const asp_kv* kv, const int32_t* idx,
                         const int32_t* count, int C, const int32_t* tail_begin, int max_tail, void* out,
-                        void* workspace, size_t workspace_bytes, asp::AttendPlan* plan, int ctas_per_sm = 0) {
-  asp_status st = check_kv(kv, true);
+                        void* workspace, size_t workspace_bytes, asp::AttendPlan* plan, int ctas_per_sm = 0,
+                        asp::FlatPlan* flat = nullptr) {
+  asp_status st = check_kv(kv, true, flat != nullptr);
   if (st != ASP_OK) return st;
   if (!q || !out) return ASP_ERR_INVALID_ARG;
   if (q_dtype != ASP_F32 && q_dtype != ASP_BF16) return ASP_ERR_INVALID_ARG;
@@ -176,23 +230,50 @@ asp_status check_attend(const void* q, asp_dtype q_dtype, int n_q_heads, const a
   if (mt < 0 || (long)C + mt < 1) return ASP_ERR_INVALID_ARG;
   if ((long)C + mt > (1L << 30)) return ASP_ERR_UNSUPPORTED;
   *plan = asp::attend_plan(kv->batch, n_q_heads, kv->n_kv_heads, kv->head_dim, C, mt, ctas_per_sm);
-  if (plan->workspace_bytes) {
-    if (!workspace || workspace_bytes < plan->workspace_bytes) return ASP_ERR_WORKSPACE;
+  size_t need = plan->workspace_bytes;
+  if (is8(kv)) {
+    *flat = flat_plan_of(kv, n_q_heads, C, mt, false, ctas_per_sm);
+    need = flat->workspace_bytes;
+  }
+  if (need) {
+    if (!workspace || workspace_bytes < need) return ASP_ERR_WORKSPACE;
     if (!aligned16(workspace)) return ASP_ERR_WORKSPACE;
   }
   return ASP_OK;
 }
 
 asp_status check_append(const asp_kv* kv, const void* k_new, const void* v_new, const void* meta, int quest_page) {
-  asp_status st = check_kv(kv, true);
+  asp_status st = check_kv(kv, true, true);
   if (st != ASP_OK) return st;
   if (!k_new || !v_new || !kv->seq_lens) return ASP_ERR_INVALID_ARG;
   if (!aligned16(k_new) || !aligned16(v_new)) return ASP_ERR_INVALID_ARG;
+  if (is8(kv)) {
+    if (!is_wide(kv->src_dtype)) return ASP_ERR_INVALID_ARG;
+    if (meta) return ASP_ERR_UNSUPPORTED;
+  }
   if (meta) {
     if (quest_page <= 0 || !aligned16(meta)) return ASP_ERR_INVALID_ARG;
     if (quest_page % 16 || quest_page > 256) return ASP_ERR_UNSUPPORTED;
     if (kv->page_size && kv->page_size != quest_page) return ASP_ERR_UNSUPPORTED;
   }
+  return ASP_OK;
+}
+
+cudaError_t append(const asp_kv* kv, const void* k_new, const void* v_new, int32_t* tail_begin, void* meta,
+                   int quest_page, cudaStream_t s) {
+  int32_t* const lens = const_cast<int32_t*>(kv->seq_lens);
+  if (is8(kv)) return asp::launch_append8(view_of(kv), k_new, v_new, kv->src_dtype == ASP_F32, lens, tail_begin, s);
+  return asp::launch_append(view_of(kv), k_new, v_new, lens, tail_begin, meta, quest_page, s);
+}
+
+asp_status check_rows8(const asp_kv* kv, const void* k, const void* v, asp_dtype dtype, int64_t sb, int64_t sh,
+                       int64_t st) {
+  const asp_status e = check_kv(kv, true, true);
+  if (e != ASP_OK) return e;
+  if (!is8(kv)) return ASP_ERR_UNSUPPORTED;
+  if (!k || !v || !aligned16(k) || !aligned16(v) || !is_wide(dtype)) return ASP_ERR_INVALID_ARG;
+  const int64_t per = dtype == ASP_F32 ? 4 : 8;   // elements of 16 bytes
+  if (sb < 0 || sh < 0 || st < 0 || sb % per || sh % per || st % per) return ASP_ERR_INVALID_ARG;
   return ASP_OK;
 }
 
@@ -229,7 +310,7 @@ asp_status asp_predict_query(float* qhist, int ring_start, const void* q_new, as
 }
 
 asp_status asp_score_keys(const float* qpred, int n_q_heads, const asp_kv* kv, float* scores, asp_stream_t stream) {
-  asp_status st = check_kv(kv, false);
+  asp_status st = check_kv(kv, false, true);
   if (st != ASP_OK) return st;
   if (!qpred || !scores) return ASP_ERR_INVALID_ARG;
   if (n_q_heads <= 0 || n_q_heads % kv->n_kv_heads) return ASP_ERR_INVALID_ARG;
@@ -289,13 +370,44 @@ size_t asp_attend_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int 
   return asp::attend_plan(batch, n_q_heads, n_kv_heads, head_dim, C, max_tail).workspace_bytes;
 }
 
+size_t asp_attend_workspace_bytes_kv(const asp_kv* kv, int n_q_heads, int C, int max_tail) {
+  if (!sizes_ok(kv, n_q_heads, C, max_tail)) return 0;
+  if (is8(kv)) return flat_plan_of(kv, n_q_heads, C, max_tail, false, 0).workspace_bytes;
+  return asp_attend_workspace_bytes(kv->batch, n_q_heads, kv->n_kv_heads, kv->head_dim, C, max_tail);
+}
+
+size_t asp_decode_workspace_bytes_kv(const asp_kv* kv, int n_q_heads, int C, int max_tail) {
+  if (!sizes_ok(kv, n_q_heads, C, max_tail) || C < 1) return 0;
+  if (!is8(kv)) return asp_decode_workspace_bytes(kv->batch, n_q_heads, kv->n_kv_heads, kv->head_dim, C, max_tail);
+  return round256(flat_plan_of(kv, n_q_heads, C, max_tail, false, kDecodeAttendCtasPerSm).workspace_bytes) +
+         (size_t)kv->batch * kv->n_kv_heads * asp::kTopBins * 4;
+}
+
+size_t asp_accumulate_workspace_bytes(const asp_kv* kv, int n_q_heads, int C, int max_tail) {
+  if (!sizes_ok(kv, n_q_heads, C, max_tail)) return 0;
+  if (kv->kv_dtype != ASP_F32) return flat_plan_of(kv, n_q_heads, C, max_tail, true, 0).workspace_bytes;
+  return wide_accumulate(kv, n_q_heads, C, max_tail,
+                         asp::attend_plan(kv->batch, n_q_heads, kv->n_kv_heads, kv->head_dim, C, max_tail).workspace_bytes)
+      .bytes;
+}
+
+size_t asp_evict_workspace_bytes(const asp_kv* kv, int C) {
+  if (!kv || kv->batch <= 0 || kv->n_kv_heads <= 0 || C < 1 || (long)kv->batch * kv->n_kv_heads > kMaxGridY) return 0;
+  return round256((size_t)kv->batch * kv->n_kv_heads * 4);
+}
+
 asp_status asp_sparse_attend(const void* q, asp_dtype q_dtype, int n_q_heads, const asp_kv* kv, const int32_t* idx,
                              const int32_t* count, int C, const int32_t* tail_begin, int max_tail, void* out,
                              float* lse, void* workspace, size_t workspace_bytes, asp_stream_t stream) {
   asp::AttendPlan plan;
+  asp::FlatPlan flat;
   asp_status st = check_attend(q, q_dtype, n_q_heads, kv, idx, count, C, tail_begin, max_tail, out, workspace,
-                               workspace_bytes, &plan);
+                               workspace_bytes, &plan, 0, &flat);
   if (st != ASP_OK) return st;
+  if (is8(kv))
+    return cuda_status(asp::launch_attend_flat(q, q_dtype == ASP_F32, n_q_heads, view_of(kv), idx, count, C, tail_begin,
+                                               max_tail, out, lse, nullptr, workspace, flat,
+                                               reinterpret_cast<cudaStream_t>(stream)));
   return cuda_status(asp::launch_attend(q, q_dtype == ASP_F32, n_q_heads, view_of(kv), idx, count, C, tail_begin,
                                         max_tail, out, lse, workspace, plan, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -317,15 +429,89 @@ asp_status asp_sparse_attend_noalloc(const void* q, asp_dtype q_dtype, int n_q_h
                                                 reinterpret_cast<cudaStream_t>(stream)));
 }
 
+asp_status asp_attend_accumulate(const void* q, asp_dtype q_dtype, int n_q_heads, const asp_kv* kv, const int32_t* idx,
+                                 const int32_t* count, int C, const int32_t* tail_begin, int max_tail, void* out,
+                                 float* lse, float* acc, void* workspace, size_t workspace_bytes,
+                                 asp_stream_t stream) {
+  // the workspace is checked below against this call's own need
+  asp::AttendPlan plan;
+  asp::FlatPlan flat;
+  void* const stand_in = reinterpret_cast<void*>(static_cast<uintptr_t>(256));
+  asp_status st = check_attend(q, q_dtype, n_q_heads, kv, idx, count, C, tail_begin, max_tail, out, stand_in,
+                               ~static_cast<size_t>(0), &plan, 0, &flat);
+  if (st != ASP_OK) return st;
+  if (!acc) return ASP_ERR_INVALID_ARG;
+  const int mt = tail_begin ? max_tail : 0;
+  const size_t need = asp_accumulate_workspace_bytes(kv, n_q_heads, C, mt);
+  if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)) return ASP_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const KvView v = view_of(kv);
+  if (kv->kv_dtype != ASP_F32)
+    return cuda_status(asp::launch_attend_flat(q, q_dtype == ASP_F32, n_q_heads, v, idx, count, C, tail_begin, max_tail,
+                                               out, lse, acc, workspace,
+                                               flat_plan_of(kv, n_q_heads, C, mt, true, 0), s));
+  const WideAccumulate w = wide_accumulate(kv, n_q_heads, C, mt, plan.workspace_bytes);
+  uint8_t* const ws = static_cast<uint8_t*>(workspace);
+  if (!lse) lse = reinterpret_cast<float*>(ws + w.lse_off);
+  float* const logits = reinterpret_cast<float*>(ws + w.logits_off);
+  cudaError_t e = asp::launch_attend_logits(q, q_dtype == ASP_F32, n_q_heads, v, idx, count, C, tail_begin, max_tail,
+                                            out, lse, ws, plan, logits, w.row_stride, s);
+  if (e == cudaSuccess)
+    e = asp::launch_accumulate(logits, w.row_stride, lse, n_q_heads, v, idx, count, C, tail_begin, max_tail, acc, s);
+  return cuda_status(e);
+}
+
+asp_status asp_evict_kv(const asp_kv* kv, const float* acc, float* acc_out, int C, int n_sink, int n_recent,
+                        int32_t* idx, int32_t* count, void* workspace, size_t workspace_bytes, asp_stream_t stream) {
+  asp_status st = check_kv(kv, true, true);
+  if (st != ASP_OK) return st;
+  if (!kv->seq_lens || !acc || !acc_out || !idx || !count) return ASP_ERR_INVALID_ARG;
+  if (C < 1 || n_sink < 0 || n_recent < 0 || (long)n_sink + n_recent > C) return ASP_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < asp_evict_workspace_bytes(kv, C) || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return ASP_ERR_WORKSPACE;
+  asp::EvictArgs a;
+  a.acc = acc;
+  a.acc_out = acc_out;
+  a.C = C;
+  a.n_sink = n_sink;
+  a.n_recent = n_recent;
+  a.idx = idx;
+  a.count = count;
+  a.keep_len = static_cast<int32_t*>(workspace);
+  return cuda_status(asp::launch_evict(view_of(kv), const_cast<int32_t*>(kv->seq_lens), a,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+asp_status asp_quantize_kv(const asp_kv* kv, const void* k_src, const void* v_src, asp_dtype src_dtype,
+                           int64_t stride_batch, int64_t stride_head, int64_t stride_token, asp_stream_t stream) {
+  const asp_status st = check_rows8(kv, k_src, v_src, src_dtype, stride_batch, stride_head, stride_token);
+  if (st != ASP_OK) return st;
+  return cuda_status(asp::launch_quantize(view_of(kv), k_src, v_src, src_dtype == ASP_F32,
+                                          asp::Strides3{stride_batch, stride_head, stride_token},
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+asp_status asp_dequantize_kv(const asp_kv* kv, void* k_dst, void* v_dst, asp_dtype dst_dtype, int64_t stride_batch,
+                             int64_t stride_head, int64_t stride_token, asp_stream_t stream) {
+  const asp_status st = check_rows8(kv, k_dst, v_dst, dst_dtype, stride_batch, stride_head, stride_token);
+  if (st != ASP_OK) return st;
+  return cuda_status(asp::launch_dequantize(view_of(kv), k_dst, v_dst, dst_dtype == ASP_F32,
+                                            asp::Strides3{stride_batch, stride_head, stride_token},
+                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
 asp_status asp_decode_step(const asp_decode_args* a) {
   if (!a) return ASP_ERR_INVALID_ARG;
   asp::AttendPlan plan;
+  asp::FlatPlan flat;
   asp_status st = check_attend(a->q_t, a->q_dtype, a->n_q_heads, a->kv, a->idx_cur, a->count_cur, a->C, a->tail_begin,
-                               a->max_tail, a->out, a->workspace, a->workspace_bytes, &plan, kDecodeAttendCtasPerSm);
+                               a->max_tail, a->out, a->workspace, a->workspace_bytes, &plan, kDecodeAttendCtasPerSm, &flat);
   if (st != ASP_OK) return st;
   if (a->C < 1 || !a->qhist || !a->qpred || !a->scores || !a->idx_next || !a->count_next) return ASP_ERR_INVALID_ARG;
   const int mt = a->tail_begin ? a->max_tail : 0;
-  const size_t hist_off = decode_hist_offset(a->kv->batch, a->n_q_heads, a->kv->n_kv_heads, a->kv->head_dim, a->C, mt);
+  const size_t hist_off =
+      is8(a->kv) ? round256(flat.workspace_bytes)
+                 : decode_hist_offset(a->kv->batch, a->n_q_heads, a->kv->n_kv_heads, a->kv->head_dim, a->C, mt);
   const size_t hist_words = (size_t)a->kv->batch * a->kv->n_kv_heads * asp::kTopBins;
   if (!a->workspace || a->workspace_bytes < hist_off + hist_words * 4 ||
       (reinterpret_cast<uintptr_t>(a->workspace) & 255))
@@ -374,15 +560,17 @@ asp_status asp_decode_step(const asp_decode_args* a) {
   cudaError_t e = cudaStreamIsCapturing(sm, &capture);
   if (e == cudaSuccess && capture == cudaStreamCaptureStatusNone) e = cudaStreamWaitEvent(sm, done, 0);
   if (e == cudaSuccess && a->k_new)   // before the fork: both streams see the new token
-    e = asp::launch_append(kv, a->k_new, a->v_new, const_cast<int32_t*>(a->kv->seq_lens),
-                           const_cast<int32_t*>(a->tail_begin), a->quest_meta, a->quest_page, sm);
+    e = append(a->kv, a->k_new, a->v_new, const_cast<int32_t*>(a->tail_begin), a->quest_meta, a->quest_page, sm);
   if (e == cudaSuccess) e = cudaEventRecord(fork, sm);
   // main stream: attention of this step, issued first so that its CTAs (one per
   // SM) are placed before the side chain's, in a captured graph as in a stream
   if (e == cudaSuccess) e = mark(6, sm);
   if (e == cudaSuccess)
-    e = asp::launch_attend(a->q_t, a->q_dtype == ASP_F32, a->n_q_heads, kv, a->idx_cur, a->count_cur, a->C,
-                           a->tail_begin, a->max_tail, a->out, a->lse, a->workspace, plan, sm);
+    e = kv.kv8 ? asp::launch_attend_flat(a->q_t, a->q_dtype == ASP_F32, a->n_q_heads, kv, a->idx_cur, a->count_cur,
+                                         a->C, a->tail_begin, a->max_tail, a->out, a->lse, nullptr, a->workspace, flat,
+                                         sm)
+               : asp::launch_attend(a->q_t, a->q_dtype == ASP_F32, a->n_q_heads, kv, a->idx_cur, a->count_cur, a->C,
+                                    a->tail_begin, a->max_tail, a->out, a->lse, a->workspace, plan, sm);
   if (e == cudaSuccess) e = mark(7, sm);
   // out and lse are complete here: a caller may read them back from this point on
   if (e == cudaSuccess && a->ev_attend_done)
@@ -478,8 +666,8 @@ asp_status asp_append_kv(const asp_kv* kv, const void* k_new, const void* v_new,
                          void* quest_meta, int quest_page, asp_stream_t stream) {
   asp_status st = check_append(kv, k_new, v_new, quest_meta, quest_page);
   if (st != ASP_OK) return st;
-  return cuda_status(asp::launch_append(view_of(kv), k_new, v_new, const_cast<int32_t*>(kv->seq_lens), tail_begin_out,
-                                        quest_meta, quest_page, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(append(kv, k_new, v_new, tail_begin_out, quest_meta, quest_page,
+                            reinterpret_cast<cudaStream_t>(stream)));
 }
 
 asp_status asp_quest_build_meta(const asp_kv* kv, int quest_page, void* meta, asp_stream_t stream) {
@@ -556,6 +744,10 @@ asp_status asp_device_status(asp_stream_t stream, int32_t* bits_out) {
   if (e == cudaSuccess) e = asp::read_status_quest(s, &v);
   if (e == cudaSuccess) e = asp::read_status_score_tc(s, &v);
   if (e == cudaSuccess) e = asp::read_status_append(s, &v);
+  if (e == cudaSuccess) e = asp::read_status_cache8(s, &v);
+  if (e == cudaSuccess) e = asp::read_status_score8(s, &v);
+  if (e == cudaSuccess) e = asp::read_status_attend_flat(s, &v);
+  if (e == cudaSuccess) e = asp::read_status_evict(s, &v);
   if (bits_out) *bits_out = v;
   if (e != cudaSuccess) return ASP_ERR_CUDA;
   return v ? ASP_ERR_DEVICE : ASP_OK;

@@ -62,9 +62,12 @@ struct AttParams {
   void* out;
   float* lse;
   float qscale;   // log2(e) / sqrt(d)
+  float* logits;  // attend_kernel with LOGITS: [units][G][logits_stride], base 2
+  int logits_stride;
 };
 
-template <typename KT, int D, int G, int STAGES>
+// LOGITS: every row's logits are also left in p.logits (-inf for rows not attended).
+template <typename KT, int D, int G, int STAGES, bool LOGITS = false>
 __global__ void __launch_bounds__(kWarps * 32) attend_kernel(AttParams p) {
   using E = Elem<KT>;
   constexpr int ROW_BYTES = D * E::kBytes;
@@ -279,6 +282,8 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(AttParams p) {
       for (int k = 0; k < RPL; ++k) {
         const int row = rl + k * LPG;
         x[k] = (row < kTile && ((vm >> row) & 1u)) ? lg[row * G + g] : -INFINITY;
+        if (LOGITS && row < kTile)
+          p.logits[((size_t)unit * G + g) * p.logits_stride + r0 + (warp + t * kWarps) * kTile + row] = x[k];
         mloc = fmaxf(mloc, x[k]);
       }
 #pragma unroll
@@ -1312,12 +1317,12 @@ __global__ void __launch_bounds__(D) attend_merge_kernel(const float* __restrict
   if (c == 0 && lse) lse[bh] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
 }
 
-template <typename KT, int D, int G>
+template <typename KT, int D, int G, bool LOGITS = false>
 cudaError_t launch_t(const AttParams& p, cudaStream_t s) {
   constexpr int ROW_BYTES = D * Elem<KT>::kBytes;
   constexpr int TILE_BYTES = 2 * kTile * ROW_BYTES;
   constexpr int STAGES = 2;
-  auto kern = attend_kernel<KT, D, G, STAGES>;
+  auto kern = attend_kernel<KT, D, G, STAGES, LOGITS>;
   size_t smem = (size_t)kWarps * STAGES * TILE_BYTES + kWarps * STAGES * 8 + (size_t)kWarps * (kTile * G + G) * 4;
   const size_t merge = (size_t)kWarps * G * (D + 2) * 4;
   if (smem < merge) smem = merge;
@@ -1367,13 +1372,13 @@ cudaError_t dispatch_mma(int G, const AttParams& p, cudaStream_t s) {
   }
 }
 
-template <typename KT, int D>
+template <typename KT, int D, bool LOGITS = false>
 cudaError_t dispatch_g(int G, const AttParams& p, cudaStream_t s) {
   switch (G) {
-    case 1: return launch_t<KT, D, 1>(p, s);
-    case 2: return launch_t<KT, D, 2>(p, s);
-    case 4: return launch_t<KT, D, 4>(p, s);
-    case 8: return launch_t<KT, D, 8>(p, s);
+    case 1: return launch_t<KT, D, 1, LOGITS>(p, s);
+    case 2: return launch_t<KT, D, 2, LOGITS>(p, s);
+    case 4: return launch_t<KT, D, 4, LOGITS>(p, s);
+    case 8: return launch_t<KT, D, 8, LOGITS>(p, s);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -1509,10 +1514,12 @@ cudaError_t dispatch_gather(int G, const AttParams& p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_attend(const void* q, int q_f32, int n_q_heads, const KvView& kv, const int32_t* idx,
-                          const int32_t* count, int C, const int32_t* tail_begin, int max_tail, void* out,
-                          float* lse, void* workspace, const AttendPlan& plan, cudaStream_t s) {
+static AttParams attend_params(const void* q, int q_f32, int n_q_heads, const KvView& kv, const int32_t* idx,
+                               const int32_t* count, int C, const int32_t* tail_begin, int max_tail, void* out,
+                               float* lse, void* workspace, const AttendPlan& plan, bool gather) {
   AttParams p;
+  p.logits = nullptr;
+  p.logits_stride = 0;
   p.q = q;
   p.q_f32 = q_f32;
   p.n_q_heads = n_q_heads;
@@ -1539,7 +1546,6 @@ cudaError_t launch_attend(const void* q, int q_f32, int n_q_heads, const KvView&
   p.tiles_per_unit = plan.tiles_per_unit;
   p.total_tiles = (long long)kv.batch * kv.n_kv * plan.tiles_per_unit;
   p.stages = 0;
-  const bool gather = plan.gather && !kv.kv_f32 && !q_f32 && (reinterpret_cast<uintptr_t>(q) & 15) == 0;
   if (gather) {
     p.ctas = plan.gather_ctas > 0 ? plan.gather_ctas : 1;
     const size_t slots = 2 * (size_t)p.ctas * (n_q_heads / kv.n_kv);
@@ -1557,11 +1563,32 @@ cudaError_t launch_attend(const void* q, int q_f32, int n_q_heads, const KvView&
   p.out = out;
   p.lse = lse;
   p.qscale = kLog2e / sqrtf((float)kv.head_dim);
+  return p;
+}
+
+cudaError_t launch_attend(const void* q, int q_f32, int n_q_heads, const KvView& kv, const int32_t* idx,
+                          const int32_t* count, int C, const int32_t* tail_begin, int max_tail, void* out,
+                          float* lse, void* workspace, const AttendPlan& plan, cudaStream_t s) {
+  const bool gather = plan.gather && !kv.kv_f32 && !q_f32 && (reinterpret_cast<uintptr_t>(q) & 15) == 0;
+  const AttParams p = attend_params(q, q_f32, n_q_heads, kv, idx, count, C, tail_begin, max_tail, out, lse, workspace,
+                                    plan, gather);
   const int G = n_q_heads / kv.n_kv;
   if (gather) return kv.head_dim == 64 ? dispatch_gather<64>(G, p, s) : dispatch_gather<128>(G, p, s);
   if (kv.kv_f32) return kv.head_dim == 64 ? dispatch_g<float, 64>(G, p, s) : dispatch_g<float, 128>(G, p, s);
   if (!q_f32) return kv.head_dim == 64 ? dispatch_mma<64>(G, p, s) : dispatch_mma<128>(G, p, s);
   return kv.head_dim == 64 ? dispatch_g<__nv_bfloat16, 64>(G, p, s) : dispatch_g<__nv_bfloat16, 128>(G, p, s);
+}
+
+cudaError_t launch_attend_logits(const void* q, int q_f32, int n_q_heads, const KvView& kv, const int32_t* idx,
+                                 const int32_t* count, int C, const int32_t* tail_begin, int max_tail, void* out,
+                                 float* lse, void* workspace, const AttendPlan& plan, float* logits, int row_stride,
+                                 cudaStream_t s) {
+  AttParams p = attend_params(q, q_f32, n_q_heads, kv, idx, count, C, tail_begin, max_tail, out, lse, workspace, plan,
+                              false);
+  p.logits = logits;
+  p.logits_stride = row_stride;
+  const int G = n_q_heads / kv.n_kv;
+  return kv.head_dim == 64 ? dispatch_g<float, 64, true>(G, p, s) : dispatch_g<float, 128, true>(G, p, s);
 }
 
 // Scratch of asp_sparse_attend_noalloc: the split-K partials of one call, for

@@ -95,6 +95,10 @@ cudaError_t read_status_attend(cudaStream_t s, int* bits);
 cudaError_t read_status_quest(cudaStream_t s, int* bits);
 cudaError_t read_status_score_tc(cudaStream_t s, int* bits);
 cudaError_t read_status_append(cudaStream_t s, int* bits);
+cudaError_t read_status_cache8(cudaStream_t s, int* bits);
+cudaError_t read_status_score8(cudaStream_t s, int* bits);
+cudaError_t read_status_attend_flat(cudaStream_t s, int* bits);
+cudaError_t read_status_evict(cudaStream_t s, int* bits);
 
 // ---- step 1 -----------------------------------------------------------------
 struct PredictArgs {
@@ -132,7 +136,12 @@ size_t predict_factor_bytes(int n_heads, int wmax);
 struct KvView {
   const void* k;
   const void* v;
-  int kv_f32;             // 1: fp32, 0: bf16
+  int kv_f32;             // 1: fp32, 0: bf16 (or 8 bits, see kv8)
+  int kv8;                // 0: wide values; 1: E4M3 codes; 2: I8 codes
+  float* k_scale;         // kv8: fp32 per block of 2^block_shift tokens, KV head and side
+  float* v_scale;
+  int block_shift;
+  int blocks_per_row;     // kv8: blocks of a sequence (contiguous) or of a page (paged)
   int batch, n_kv, head_dim, t_max;
   int page_size, max_pages, n_pages;
   const int32_t* page_table;
@@ -143,6 +152,20 @@ struct KvView {
 // page bounds [batch, n_kv, ceil(t_max / quest_page), 2, head_dim] kept current.
 cudaError_t launch_append(const KvView& kv, const void* k_new, const void* v_new, int32_t* seq_lens,
                           int32_t* tail_begin, void* meta, int quest_page, cudaStream_t s);
+
+// 8-bit caches: the prompt's rows into codes and scales, and back.
+struct Strides3 {
+  int64_t batch, head, token;   // elements
+};
+cudaError_t launch_quantize(const KvView& kv, const void* k_src, const void* v_src, int src_f32, Strides3 st,
+                            cudaStream_t s);
+cudaError_t launch_dequantize(const KvView& kv, void* k_dst, void* v_dst, int dst_f32, Strides3 st, cudaStream_t s);
+// The new token's rows (fp32 or bf16) into an 8-bit cache; as launch_append otherwise.
+cudaError_t launch_append8(const KvView& kv, const void* k_new, const void* v_new, int src_f32, int32_t* seq_lens,
+                           int32_t* tail_begin, cudaStream_t s);
+// The key scan of an 8-bit cache (hist as below).
+cudaError_t launch_score8(const float* qpred, int n_q_heads, const KvView& kv, float* scores, cudaStream_t s,
+                          int32_t* hist = nullptr);
 
 // hist: optional [batch * n_kv, 2048] int32 counts of the scores' top 11 key bits
 // (must be zero on entry); the selection then skips its own first pass.
@@ -182,6 +205,9 @@ struct SelectArgs {
   int32_t* idx;
   int32_t* count;
   const int32_t* hist0;      // optional first-pass histogram [n_rows, 2048] (expand == 1 only)
+  int n_sink = 0;            // eviction (keep_len set): a row's first n_sink and last n_recent tokens always chosen
+  int n_recent = 0;
+  int32_t* keep_len = nullptr;   // optional [n_rows]: the row's length, for the kernel that moves the rows
   int key_cap;               // set by launch_select: shared-memory slots per row (keys, or packed lists)
 };
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t s);
@@ -204,12 +230,50 @@ AttendPlan attend_plan(int batch, int n_q_heads, int n_kv_heads, int head_dim, i
 cudaError_t launch_attend(const void* q, int q_f32, int n_q_heads, const KvView& kv, const int32_t* idx,
                           const int32_t* count, int C, const int32_t* tail_begin, int max_tail, void* out,
                           float* lse, void* workspace, const AttendPlan& plan, cudaStream_t s);
+// The same for an fp32 cache (plan made with ctas_per_sm 0), leaving the logits (base 2;
+// -inf for rows not attended) in logits [batch * n_kv, G, row_stride].
+cudaError_t launch_attend_logits(const void* q, int q_f32, int n_q_heads, const KvView& kv, const int32_t* idx,
+                                 const int32_t* count, int C, const int32_t* tail_begin, int max_tail, void* out,
+                                 float* lse, void* workspace, const AttendPlan& plan, float* logits, int row_stride,
+                                 cudaStream_t s);
 
 // Launches step 4 with its split-K partials in the library's fixed scratch array
 // (asp_sparse_attend_noalloc); `plan.workspace_bytes` must fit in it.
 cudaError_t launch_attend_noalloc(const void* q, int q_f32, int n_q_heads, const KvView& kv, const int32_t* idx,
                                   const int32_t* count, int C, const int32_t* tail_begin, int max_tail, void* out,
                                   float* lse, const AttendPlan& plan, cudaStream_t s);
+
+// ---- step 4 with equal shares of rows per CTA ------------------------------------
+// Attention of an 8-bit cache, and of a bf16 or 8-bit cache with the weights summed per
+// token (accumulate).
+struct FlatPlan {
+  int ctas;            // CTAs of the attention kernel
+  int whole;           // 1: one CTA per (sequence, KV head), nothing to merge
+  int row_stride;      // accumulate: logits per head and unit
+  size_t part_off, info_off, logits_off;   // byte offsets in the workspace
+  size_t workspace_bytes;
+};
+// ctas_per_sm: 0 for a stand-alone call, 1 beside the key scan in the decode step.
+FlatPlan flat_plan(int batch, int n_q_heads, int n_kv_heads, int head_dim, int C, int max_tail, bool kv8,
+                   bool accumulate, int ctas_per_sm);
+cudaError_t launch_attend_flat(const void* q, int q_f32, int n_q_heads, const KvView& kv, const int32_t* idx,
+                               const int32_t* count, int C, const int32_t* tail_begin, int max_tail, void* out,
+                               float* lse, float* acc, void* workspace, const FlatPlan& plan, cudaStream_t s);
+// acc of an fp32 cache from the logits that attend_kernel left and the final lse.
+cudaError_t launch_accumulate(const float* logits, int row_stride, const float* lse, int n_q_heads, const KvView& kv,
+                              const int32_t* idx, const int32_t* count, int C, const int32_t* tail_begin, int max_tail,
+                              float* acc, cudaStream_t s);
+
+// ---- eviction ---------------------------------------------------------------------
+struct EvictArgs {
+  const float* acc;
+  float* acc_out;
+  int C, n_sink, n_recent;
+  int32_t* idx;
+  int32_t* count;
+  int32_t* keep_len;   // workspace [batch * n_kv]
+};
+cudaError_t launch_evict(const KvView& kv, int32_t* seq_lens, const EvictArgs& a, cudaStream_t s);
 
 // ---- failure detection ----------------------------------------------------------
 // One warp waits on a barrier nothing arrives on, bounded to `tries` attempts;

@@ -56,8 +56,11 @@ __device__ __forceinline__ float4 ld_issue(const float4* p) {
 
 // FUSED: the first digit's histogram is given and the scores load as 16-byte
 // vectors (the decode step's case); that kernel carries no code for the others.
-template <bool FUSED>
+// KEEP (eviction): the first n_sink and last n_recent tokens of a row count above every
+// score, and the row's length goes to keep_len.
+template <bool FUSED, bool KEEP = false>
 __global__ void __launch_bounds__(kThreads, 1) select_kernel(SelectArgs a) {
+  static_assert(!(FUSED && KEEP), "the given histogram counts plain scores");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x;
   const int b = row / a.rows_per_seq;
@@ -81,6 +84,12 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(SelectArgs a) {
       const int tok = u * E + e;
       out[pos * E + e] = tok < T ? tok : -1;
     }
+  };
+
+  if (KEEP && tid == 0) a.keep_len[row] = T;
+  auto key_of = [&](int i, float score) -> uint32_t {   // unit i's key
+    if (KEEP && (i < a.n_sink || i >= n - a.n_recent)) return 0xffffffffu;
+    return order_key(score);
   };
 
   if (n <= a.c_units) {   // every unit chosen
@@ -118,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(SelectArgs a) {
     return;
   }
   const bool keys_in_smem = cached && !fused;   // the key array is built (else keys are re-read from L2)
-  auto key_at = [&](int i) -> uint32_t { return keys_in_smem ? keys[i] : order_key(srow[i]); };
+  auto key_at = [&](int i) -> uint32_t { return keys_in_smem ? keys[i] : key_of(i, srow[i]); };
   if (!fused && cached && vec) {
     const int n4 = (n + 3) >> 2;
     constexpr int U = 4;           // vectors per thread in flight
@@ -132,7 +141,8 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(SelectArgs a) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i4 = base + u * kThreads + tid;
-        const uint32_t k4[4] = {order_key(f[u].x), order_key(f[u].y), order_key(f[u].z), order_key(f[u].w)};
+        const uint32_t k4[4] = {key_of(4 * i4, f[u].x), key_of(4 * i4 + 1, f[u].y), key_of(4 * i4 + 2, f[u].z),
+                                key_of(4 * i4 + 3, f[u].w)};
         nan_seen |= i4 < n4 && (isnan(f[u].x) || isnan(f[u].y) || isnan(f[u].z) || isnan(f[u].w));
         if (i4 < n4) *reinterpret_cast<uint4*>(&keys[4 * i4]) = make_uint4(k4[0], k4[1], k4[2], k4[3]);
         if (own_h0) {
@@ -148,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(SelectArgs a) {
       if (i < n) {
         const float sv = srow[i];
         nan_seen |= isnan(sv);
-        key = order_key(sv);
+        key = key_of(i, sv);
         if (cached) keys[i] = key;
       }
       if (own_h0) count_digit(h0, i < n, key >> kTopShift);
@@ -378,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(SelectArgs a) {
   // are few).
   auto packed_key = [&](uint32_t e, int k) -> uint32_t {
     if (e & kGtTag) return 0xffffffffu;
-    return kcache ? keys[pe - 1 - k] : order_key(srow[e]);
+    return kcache ? keys[pe - 1 - k] : key_of((int)e, srow[e]);
   };
 
   // ---- second (11 bits) and third (10 bits) digits
@@ -738,6 +748,11 @@ cudaError_t launch_select(const SelectArgs& a, cudaStream_t s) {
   // shared-memory slots for keys or packed lists; the same for every row
   args.key_cap = len_max <= kSmemKeys ? ((len_max + 3) & ~3) : kSmemKeys;
   const size_t smem = (size_t)(args.key_cap > 0 ? args.key_cap : 4) * 4;
+  if (a.keep_len) {   // eviction: no histogram comes with the sums
+    auto keep = select_kernel<false, true>;
+    if (prepare_kernel((const void*)keep, smem, kThreads) < 1) return cudaErrorInvalidConfiguration;
+    return launch_pdl(keep, dim3(args.n_rows), dim3(kThreads), smem, s, args);
+  }
   const bool fused = a.hist0 != nullptr && (a.row_stride & 3) == 0 &&
                      (reinterpret_cast<uintptr_t>(a.scores) & 15) == 0 && args.key_cap >= kWarps * 4;
   if (fused && a.expand == 1 && a.t_max <= kRegMaxUnits) {
