@@ -10,13 +10,16 @@
 //    shared by CTAs leaves a partial (m, l, M, unnormalised output) per CTA in the workspace
 //    and finish_kernel joins them.  With few rows per unit a CTA takes a whole unit instead
 //    and nothing is joined.
-//  * A warp owns every 8th tile of its CTA's range and a ring of two stages: rows come in
-//    by 16-byte cp.async, swizzled so that the fragment loads below meet no bank twice.
-//  * S^T[head x row] = Q . K^T and O^T[channel x head] = V^T . P by mma.m16n8k16.  A pair of
-//    codes becomes an fp16x2 operand register exactly; V's pairs run along the rows, taken
-//    by a byte permute from two rows' words, so nothing is transposed through shared memory.
-//    Heads fill 8 of the 16 rows of Q's fragments; for an fp32 query the other 8 hold the
-//    second fp16 part.  The accumulator of S^T is already the operand P.
+//  * A warp owns every W-th tile of its CTA's range and a ring of two stages, and fetches for
+//    itself in three steps that each have a whole tile's work to arrive in: the raw indices,
+//    then the pages, then the rows by 16-byte cp.async, swizzled so that the fragment loads
+//    below meet no bank twice.  (Three producer warps for twelve consumers took 196 us where
+//    this takes about 100: a tile's fetch is a quarter of its instructions, and three warps
+//    issue them too slowly.)
+//  * S[row x head] = K . Q^T and O^T[channel x head] = V^T . P by mma.m16n8k16.  A pair of codes
+//    becomes an fp16x2 operand register exactly; V's pairs run along the rows, taken by a
+//    byte permute from two rows' words, so V is not transposed through shared memory; P is, in
+//    registers, by movmatrix.  An fp32 query has a second fp16 part, one more product each.
 //  * K's scale multiplies the fp32 logits.  V's scale s = mant * 2^e multiplies the weight
 //    before it is rounded to fp16: w = 2^(x + e - M + 14) mant with M = ceil(max(x + e)),
 //    an integer like m, so rescaling is exact and no pair of scales leaves fp16's range.
@@ -29,13 +32,16 @@ namespace asp {
 namespace {
 
 constexpr int kTile = 16;
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 2;
+constexpr int kMinTiles = 8;               // of a CTA's range
+constexpr int kFlatSms = 148;
+constexpr int kMaxCtas = 2 * kFlatSms;     // of a launch that cuts units
+constexpr int kFinThreads = 256;           // finish_kernel, accumulate_kernel
 constexpr int kWBias = 14;      // the largest weight is below 2^15 before its rounding to fp16
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kNone = 0xffffffffu;
+constexpr float kLowest = -3e38f;   // a maximum before any row: finite, so that no difference is inf - inf
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -46,6 +52,7 @@ __device__ __forceinline__ float ex2(float x) {
 struct FlatParams {
   const void* q;
   int q_f32;
+  int q_aligned;         // q on a 16-byte boundary
   int n_q_heads, G;
   const uint8_t* k;
   const uint8_t* v;
@@ -53,6 +60,7 @@ struct FlatParams {
   const float* v_scale;
   int block_shift, blocks_per_row;
   int units, n_kv, t_max, page_size, max_pages, n_pages;
+  uint32_t page_magic;   // 2^32 / (page_size / 16), rounded up; 0 for pages of 16
   const int32_t* page_table;
   const int32_t* seq_lens;
   const int32_t* idx;
@@ -109,6 +117,8 @@ template <typename CT>
 struct Fmt {   // 8-bit codes, fp16 products
   static constexpr int kEB = 1;
   static constexpr bool kScaled = true;
+  static constexpr int kWarps = 8, kCtas = 2;    // of a CTA; CTAs per SM
+  static constexpr int kMergeHeads = 8;          // heads joined together at a unit's end
   __device__ __forceinline__ static void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -129,6 +139,8 @@ template <>
 struct Fmt<__nv_bfloat16> {
   static constexpr int kEB = 2;
   static constexpr bool kScaled = false;
+  static constexpr int kWarps = 12, kCtas = 1;
+  static constexpr int kMergeHeads = 4;          // shared memory holds the stages and no more
   __device__ __forceinline__ static void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -144,7 +156,12 @@ struct Fmt<__nv_bfloat16> {
   __device__ __forceinline__ static float2 unpack(uint32_t w) { return bf16x2_to_float2(w); }
 };
 
-// Stage: K rows, V rows (swizzled 16-byte chunks), then K and V scales and the row mask.
+static_assert(kFlatSms * Fmt<CodeE4M3>::kCtas <= kMaxCtas && kFlatSms * Fmt<__nv_bfloat16>::kCtas <= kMaxCtas, "join");
+
+// Stage: K rows, V rows (16-byte chunks, chunk c of row r at c ^ swz(r)), then K and V scales
+// and the row mask.  The loads of a quarter warp (half warp for 8-byte loads) fall in
+// distinct banks: K's touch rows g and g + 1 at the chunks 2t, V's the rows 2t at the chunks
+// of two lanes g (64-byte rows: K's both halves of a row pair; V's meet twice).
 template <typename CT, int D>
 struct Stage {
   static constexpr int ROW = D * Fmt<CT>::kEB;      // bytes of a row
@@ -153,41 +170,87 @@ struct Stage {
   static constexpr int SCALES = 2 * HALF;           // 16 + 16 floats
   static constexpr int MASK = SCALES + (Fmt<CT>::kScaled ? 2 * kTile * 4 : 0);
   static constexpr int BYTES = MASK + 16;
-  // The fragment loads of a quarter (half) warp fall in distinct banks: K's touch rows g,
-  // g + 1 at 4 chunks, V's the rows 2t at the chunks of two (four) lanes g.
-  __device__ __forceinline__ static int k_swz(int r) { return CH >= 8 ? (r & 1) << 2 : 0; }
-  __device__ __forceinline__ static int v_swz(int r) {
-    if constexpr (CH == 16) return ((r >> 1) & 1) | (((r >> 2) & 1) << 2);
-    else if constexpr (CH == 8) return ((r >> 1) & 3) << 1;
-    else return ((r >> 1) & 1) << 1;
+  static constexpr bool SMALL = CH == 4;
+  __device__ __forceinline__ static constexpr int swz(int r) { return SMALL ? ((r >> 1) & 1) << 1 : r & 7; }
+  // chunk of K that lane t takes in load i
+  __device__ __forceinline__ static constexpr int k_chunk(int i, int t) {
+    return SMALL ? t : 2 * t + (i & 1) + 8 * (i >> 1);
+  }
+  // channel of element e of m-tile i at lane g, and of element c of k-step ks at lane t
+  __device__ __forceinline__ static constexpr int v_chan(int i, int g, int e) {
+    return Fmt<CT>::kEB == 1 ? (D / 8) * g + 2 * i + e : (i >> 2) * 64 + 8 * g + 2 * (i & 3) + e;
+  }
+  __device__ __forceinline__ static constexpr int k_chan(int ks, int t, int c) {
+    return Fmt<CT>::kEB == 1 ? 16 * k_chunk(ks >> 2, t) + 4 * (ks & 3) + c : 8 * k_chunk(ks >> 1, t) + 4 * (ks & 1) + c;
   }
 };
 
-constexpr int mo_stride(int D) { return D + 4; }
+__host__ __device__ constexpr int mo_stride(int D) { return D + 4; }
+template <typename CT>
+__host__ __device__ constexpr int merge_heads(int G) { return G < Fmt<CT>::kMergeHeads ? G : Fmt<CT>::kMergeHeads; }
 template <typename CT, int D>
 constexpr size_t flat_smem(int G) {
-  return (size_t)kWarps * kStages * Stage<CT, D>::BYTES + (size_t)kWarps * G * mo_stride(D) * 4 + (size_t)kWarps * G * 4 * 4;
+  return (size_t)Fmt<CT>::kWarps * (kStages * Stage<CT, D>::BYTES + (merge_heads<CT>(G) * mo_stride(D) + 4 * G) * 4);
+}
+
+// acc of the rows r, r + kFinThreads, ... (VECS of them, below r1): the weights of the group's
+// heads, each from its logit by `weight`.  Rows that were not attended hold -inf.
+constexpr int kAccVecs = 4;
+constexpr int kAccRows = kAccVecs * kFinThreads;
+
+template <int VECS, typename W>
+__device__ __forceinline__ void add_weights(const FlatParams& p, int u, const UnitRows& ur, int r, int r1, W weight) {
+  float x[VECS][8];
+  int tok[VECS];
+#pragma unroll
+  for (int k = 0; k < VECS; ++k) {
+    const int rk = r + k * kFinThreads;
+    tok[k] = -1;
+    if (rk >= r1) continue;
+    tok[k] = rk < ur.n_sel ? p.idx[(size_t)u * p.C + rk] : ur.tb + (rk - ur.n_sel);
+#pragma unroll
+    for (int gg = 0; gg < 8; ++gg)
+      if (gg < p.G) x[k][gg] = p.logits[((size_t)u * p.G + gg) * p.row_stride + rk];
+  }
+#pragma unroll
+  for (int k = 0; k < VECS; ++k) {
+    if (tok[k] < 0 || x[k][0] == -INFINITY) continue;
+    float w = 0.f;
+#pragma unroll
+    for (int gg = 0; gg < 8; ++gg)
+      if (gg < p.G) w += weight(gg, x[k][gg]);
+    atomicAdd(p.acc + (size_t)u * p.t_max + tok[k], w);
+  }
+}
+
+// Transposes an 8x8 matrix of 16-bit values held two per lane.
+__device__ __forceinline__ uint32_t movm(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
 }
 
 // QP: parts of the query (8-bit caches: 1 for bf16, 2 for fp32; bf16 caches: 1 or 3).
 template <typename CT, int D, int QP, bool ACC>
-__global__ void __launch_bounds__(kThreads, sizeof(CT) == 1 ? 2 : 1) attend_flat_kernel(FlatParams p) {
+__global__ void __launch_bounds__(Fmt<CT>::kWarps * 32, Fmt<CT>::kCtas) attend_flat_kernel(FlatParams p) {
   using F = Fmt<CT>;
   using S = Stage<CT, D>;
+  constexpr int W = F::kWarps, THREADS = W * 32;
   constexpr int KS = D / 16;                 // k-steps of the logits
   constexpr int MT = D / 16;                 // m-tiles of the output
   constexpr bool WSPLIT = !F::kScaled || QP > 1;   // weights in two parts
 
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int run_pre[kThreads + 1];
+  __shared__ int run_pre[THREADS + 1];
   __shared__ int scan[33];
   __shared__ int s_first[2];
+  __shared__ float4 s_unit[8];               // of the unit's heads: m, l, M, 1 / (l 2^..)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int G = p.G;
+  const int G = p.G, GM = merge_heads<CT>(G);
   uint8_t* const ring = smem + (size_t)warp * kStages * S::BYTES;
-  float* const mo = reinterpret_cast<float*>(smem + (size_t)kWarps * kStages * S::BYTES);   // [warp][G][D + 4]
-  float* const mml = mo + (size_t)kWarps * G * mo_stride(D);                                // [warp][G][4]
+  float* const mo = reinterpret_cast<float*>(smem + (size_t)W * kStages * S::BYTES);   // [warp][GM][D + 4]
+  float* const mml = mo + (size_t)W * GM * mo_stride(D);                               // [warp][G][4]
 
   pdl_wait();
 
@@ -201,14 +264,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(CT) == 1 ? 2 : 1) attend_flat
     t0 = 0;
     t1 = total = unit_tiles(unit_rows(p, u0, threadIdx.x == 0));
   } else {
-    const int per = (p.units + kThreads - 1) / kThreads;   // units of a thread's run
-    cta_prefix_sum(kThreads, run_pre, [&](int i) {
+    const int per = (p.units + THREADS - 1) / THREADS;   // units of a thread's run
+    cta_prefix_sum(THREADS, run_pre, [&](int i) {
       int n = 0;
       for (int u = i * per; u < min(p.units, (i + 1) * per); ++u) n += unit_tiles(unit_rows(p, u, cta == 0));
       return n;
     }, scan);
-    total = run_pre[kThreads];
-    N = min(N, (total + kWarps - 1) / kWarps);   // a tile per warp, and no CTA without tiles
+    total = run_pre[THREADS];
+    N = min(N, (total + kMinTiles - 1) / kMinTiles);   // no CTA without tiles
     if (cta >= N) return;
     t0 = range_start(cta, total, N);
     t1 = range_start(cta + 1, total, N);
@@ -228,134 +291,189 @@ __global__ void __launch_bounds__(kThreads, sizeof(CT) == 1 ? 2 : 1) attend_flat
     tl0 = s_first[1];
   }
   const int ntl = t1 - t0;
-  const int my_n = ntl > warp ? (ntl - warp + kWarps - 1) / kWarps : 0;   // this warp's tiles
+  const int my_n = ntl > warp ? (ntl - warp + W - 1) / W : 0;   // this warp's tiles
 
-  // ---- producer side of the warp: its tiles in order, one position ahead of the copies
-  int pu = u0, ptl = tl0 + warp;
+  // ---- fetching: request() the tile's position and raw indices; resolve() its tokens and
+  // their pages; issue() the copies
+  int pu = u0, pb = u0 / p.n_kv, ph = u0 - pb * p.n_kv, ptl = tl0 + warp;
   UnitRows pr = unit_rows(p, pu, false);
   int pn = unit_tiles(pr);
-  int pj = 0;                // tiles whose index has been requested
-  int raw = 0, r_unit = 0, r_tl = 0;
-  UnitRows rr = pr;
-  auto fetch = [&]() {       // position and raw index of the next tile
-    if (pj >= my_n) return;
+  const int rr = lane & 15;
+  int asked = 0, a_tl = 0, raw = 0;
+  auto request = [&]() {
+    if (asked >= my_n) return;
     while (ptl >= pn) {
       ptl -= pn;
-      pr = unit_rows(p, ++pu, false);
+      ++pu;
+      if (++ph == p.n_kv) {
+        ph = 0;
+        ++pb;
+      }
+      pr = unit_rows(p, pu, false);
       pn = unit_tiles(pr);
     }
-    r_unit = pu;
-    r_tl = ptl;
-    rr = pr;
-    const int r = ptl * kTile + (lane & 15);
-    raw = r < pr.n_sel ? __ldg(p.idx + (size_t)pu * p.C + r) : 0;
-    ptl += kWarps;
-    ++pj;
+    a_tl = ptl;
+    if (a_tl * kTile < pr.n_sel) {
+      const int r = a_tl * kTile + rr;
+      raw = r < pr.n_sel ? __ldg(p.idx + (size_t)pu * p.C + r) : 0;
+    }
+    ptl += W;
+    ++asked;
+  };
+  // this lane's row of the resolved tile: contiguous, its row and scale; paged, its page and
+  // the row in it
+  uint32_t b_row = kNone, b_srow = 0;
+  int b_page = 0, b_h = 0, resolved = 0;
+  bool b_run = false;        // 16 rows that follow one another in memory
+  auto resolve = [&]() {
+    if (resolved >= my_n) return;
+    ++resolved;
+    const int r0 = a_tl * kTile, r = r0 + rr;
+    int tok = -1;
+    if (r < pr.n_sel) {
+      tok = raw;
+      if (tok < 0 || tok >= pr.T) {
+        if (lane < 16) flag_status(ASP_DEV_BAD_INDEX);
+        tok = -1;
+      } else if (tok >= pr.tb) {
+        tok = -1;   // covered by the tail
+      }
+    } else if (r < pr.n_rows) {
+      tok = pr.tb + (r - pr.n_sel);
+    }
+    b_run = r0 >= pr.n_sel && r0 + kTile <= pr.n_rows &&
+            (p.page_size == 0 || ((pr.tb + r0 - pr.n_sel) & (kTile - 1)) == 0);
+    b_row = kNone;
+    if (p.page_size == 0) {
+      if (tok >= 0) {
+        b_row = (uint32_t)((size_t)pu * p.t_max + tok);
+        if (F::kScaled) b_srow = (uint32_t)((size_t)pu * p.blocks_per_row + (tok >> p.block_shift));
+      }
+    } else if (tok >= 0) {   // tok / page_size: pages are 16 m tokens, m <= 16, and tok / 16 < 2^27
+      const uint32_t t16 = (uint32_t)tok >> 4;
+      const uint32_t lp = p.page_magic ? __umulhi(t16, p.page_magic) : t16;
+      b_page = __ldg(p.page_table + (size_t)pb * p.max_pages + lp);
+      b_row = (uint32_t)tok - lp * (uint32_t)p.page_size;
+      b_h = ph;
+    }
   };
   int issued = 0;
-  auto issue = [&]() {       // the fetched tile into the next stage (an empty group past the end)
+  const int lr = lane / S::CH, lc = lane % S::CH;
+  auto issue = [&]() {       // an empty group past the end
     if (issued < my_n) {
       uint8_t* const st = ring + (issued % kStages) * S::BYTES;
-      const int b = r_unit / p.n_kv, h = r_unit - b * p.n_kv;
-      const int r = r_tl * kTile + (lane & 15);
-      uint32_t row = kNone, srow = 0;
-      int tok = -1;
-      if (r < rr.n_sel) {
-        tok = raw;
-        if (tok < 0 || tok >= rr.T) {
-          if (lane < 16) flag_status(ASP_DEV_BAD_INDEX);
-          tok = -1;
-        } else if (tok >= rr.tb) {
-          tok = -1;   // covered by the tail
-        }
-      } else if (r < rr.n_rows) {
-        tok = rr.tb + (r - rr.n_sel);
-      }
-      if (tok >= 0) {
-        if (p.page_size == 0) {
-          row = (uint32_t)((size_t)r_unit * p.t_max + tok);
-          if (F::kScaled) srow = (uint32_t)((size_t)r_unit * p.blocks_per_row + (tok >> p.block_shift));
+      uint32_t row = b_row, srow = b_srow;
+      if (p.page_size && row != kNone) {
+        if (b_page < 0 || b_page >= p.n_pages) {
+          if (lane < 16) flag_status(ASP_DEV_BAD_PAGE);
+          row = kNone;
         } else {
-          const int page = __ldg(p.page_table + (size_t)b * p.max_pages + tok / p.page_size);
-          if (page < 0 || page >= p.n_pages) {
-            if (lane < 16) flag_status(ASP_DEV_BAD_PAGE);
-          } else {
-            const int in = tok % p.page_size;
-            row = (uint32_t)(((size_t)page * p.n_kv + h) * p.page_size + in);
-            if (F::kScaled) srow = (uint32_t)(((size_t)page * p.n_kv + h) * p.blocks_per_row + (in >> p.block_shift));
-          }
+          const size_t head = (size_t)b_page * p.n_kv + b_h;
+          if (F::kScaled) srow = (uint32_t)(head * p.blocks_per_row + (row >> p.block_shift));
+          row = (uint32_t)(head * p.page_size + row);
         }
       }
       const uint32_t vm = __ballot_sync(0xffffffffu, row != kNone) & 0xffffu;
-      const uint32_t base = smem_u32(st);
-      constexpr int RPI = 32 / S::CH;   // rows per warp instruction
-      const int ch = lane % S::CH;
+      if (vm) {
+        constexpr int RPI = 32 / S::CH;   // rows per warp instruction
+        const uint32_t base = smem_u32(st);
+        auto copy = [&](int i, const uint8_t* kf, const uint8_t* vf) {
+          const int ri = RPI * i + lr;
+          const uint32_t dst = base + ri * S::ROW + ((lc ^ S::swz(ri)) * 16);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(kf) : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + S::HALF), "l"(vf) : "memory");
+        };
+        if (b_run && vm == 0xffffu) {
+          const uint32_t row0 = __shfl_sync(0xffffffffu, row, 0);
+          const size_t off = (size_t)row0 * S::ROW + lane * 16;
+          const uint8_t* const kf = p.k + off;
+          const uint8_t* const vf = p.v + off;
 #pragma unroll
-      for (int i = 0; i < 32 / RPI; ++i) {
-        const int ri = RPI * i + lane / S::CH;     // 0-15 K rows, 16-31 V rows
-        const uint32_t src = __shfl_sync(0xffffffffu, row, ri & 15);
-        const bool ok = src != kNone;
-        const int sw = ch ^ (ri < 16 ? S::k_swz(ri) : S::v_swz(ri & 15));
-        const uint8_t* from = (ri < 16 ? p.k : p.v) + (ok ? (size_t)src * S::ROW + ch * 16 : 0);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + ri * S::ROW + sw * 16), "l"(from),
-                     "r"(ok ? 16 : 0)
-                     : "memory");
-      }
-      if constexpr (F::kScaled) {
-        const float* from = (lane < 16 ? p.k_scale : p.v_scale) + (row != kNone ? srow : 0u);
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(base + S::SCALES + lane * 4), "l"(from),
-                     "r"(row != kNone ? 4 : 0)
-                     : "memory");
+          for (int i = 0; i < kTile / RPI; ++i) copy(i, kf + i * 512, vf + i * 512);
+        } else {
+          // a row that is not read repeats one that is: its weight is zero, and nothing that
+          // was not written meets it
+          const int first = __ffs(vm) - 1;
+          const uint32_t fr = __shfl_sync(0xffffffffu, row, first), fs = __shfl_sync(0xffffffffu, srow, first);
+          if (row == kNone) {
+            row = fr;
+            srow = fs;
+          }
+#pragma unroll
+          for (int i = 0; i < kTile / RPI; ++i) {
+            const uint32_t src = __shfl_sync(0xffffffffu, row, RPI * i + lr);
+            const size_t off = (size_t)src * S::ROW + lc * 16;
+            copy(i, p.k + off, p.v + off);
+          }
+        }
+        if constexpr (F::kScaled) {
+          const float* from = (lane < 16 ? p.k_scale : p.v_scale) + srow;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(base + S::SCALES + lane * 4), "l"(from)
+                       : "memory");
+        }
       }
       if (lane == 0) *reinterpret_cast<uint32_t*>(st + S::MASK) = vm;
       ++issued;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-#pragma unroll
-  for (int s = 0; s < kStages; ++s) {
-    fetch();
-    issue();
-  }
-  fetch();
-
-  // ---- query fragments: row g is head g (part 0), row g + 8 its second part
-  constexpr int QR = QP == 1 ? 2 : (QP == 2 ? 4 : 6);   // registers per k-step
-  uint32_t qa[KS][QR];
-  float qfac = p.qscale;     // of head g
-  // channel of (k-step ks, element c): the order in which K's chunks arrive
-  auto chan = [&](int ks, int c) -> int {
-    if constexpr (F::kEB == 1) return (ks >> 2) * 64 + t * 16 + (ks & 3) * 4 + c;
-    else return (ks >> 1) * 32 + t * 8 + (ks & 1) * 4 + c;
-  };
+  // ---- query fragments: column g is head g
+  uint32_t qa[KS][2 * QP];
+  float qfac[2] = {p.qscale, p.qscale};     // of heads 2t and 2t + 1
   auto load_q = [&](int unit) {
     const int b = unit / p.n_kv, h = unit - b * p.n_kv;
-    const size_t off = ((size_t)b * p.n_q_heads + h * G + g) * D;
-    auto at = [&](int ch) -> float {
-      if (g >= G) return 0.f;
-      return p.q_f32 ? static_cast<const float*>(p.q)[off + ch]
-                     : __bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[off + ch]);
-    };
+    const size_t off = ((size_t)b * p.n_q_heads + h * G + (g < G ? g : 0)) * D;
+    float4 q4[KS];   // all loads before any use
+    if (p.q_f32) {
+      const float* const src = static_cast<const float*>(p.q) + off;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const float* const s4 = src + S::k_chan(ks, t, 0);
+        q4[ks] = p.q_aligned ? __ldg(reinterpret_cast<const float4*>(s4)) : make_float4(s4[0], s4[1], s4[2], s4[3]);
+      }
+    } else {
+      const __nv_bfloat16* const src = static_cast<const __nv_bfloat16*>(p.q) + off;
+      uint2 w[KS];
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const __nv_bfloat16* const s4 = src + S::k_chan(ks, t, 0);
+        if (p.q_aligned) {
+          w[ks] = __ldg(reinterpret_cast<const uint2*>(s4));
+        } else {
+          const unsigned short* const us = reinterpret_cast<const unsigned short*>(s4);
+          w[ks] = make_uint2((uint32_t)us[0] | ((uint32_t)us[1] << 16), (uint32_t)us[2] | ((uint32_t)us[3] << 16));
+        }
+      }
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const float2 lo = bf16x2_to_float2(w[ks].x), hi = bf16x2_to_float2(w[ks].y);
+        q4[ks] = make_float4(lo.x, lo.y, hi.x, hi.y);
+      }
+    }
+    if (g >= G) {
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) q4[ks] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     float up = 1.f;
     if constexpr (F::kScaled) {   // largest channel to [2^14, 2^15)
       uint32_t amax = 0u;
       bool bad = false;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) amax = max(amax, finite_abs(at(chan(ks, c)), bad));
+        amax = max(max(amax, max(finite_abs(q4[ks].x, bad), finite_abs(q4[ks].y, bad))),
+                   max(finite_abs(q4[ks].z, bad), finite_abs(q4[ks].w, bad)));
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       int e = (int)(amax >> 23) - 127;
       e = e < -112 ? -112 : e;
       up = exp2i(14 - e);
-      qfac = exp2i(e - 14) * p.qscale;
+      const float f = exp2i(e - 14) * p.qscale;
+      qfac[0] = __shfl_sync(0xffffffffu, f, 8 * t);
+      qfac[1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
     }
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      float x[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) x[c] = at(chan(ks, c)) * up;
+      float x[4] = {q4[ks].x * up, q4[ks].y * up, q4[ks].z * up, q4[ks].w * up};
 #pragma unroll
       for (int part = 0; part < QP; ++part) {
 #pragma unroll
@@ -369,9 +487,18 @@ __global__ void __launch_bounds__(kThreads, sizeof(CT) == 1 ? 2 : 1) attend_flat
       }
     }
   };
-  load_q(u0);
+  request();
+  load_q(u0);      // while the first indices arrive
+  resolve();
+  request();
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) {
+    issue();
+    resolve();
+    request();
+  }
 
-  // ---- consumer side
+  // ---- the tiles of each unit in turn
   int j = 0;                 // this warp's next tile
   int seg_t0 = t0 - tl0;     // where the current unit's tiles begin in the flattened order
   for (int u = u0;; ++u) {
@@ -379,365 +506,404 @@ __global__ void __launch_bounds__(kThreads, sizeof(CT) == 1 ? 2 : 1) attend_flat
     const int un = unit_tiles(ur);
     const int seg_end = min(t1, seg_t0 + un);
     const int kend = seg_end - t0 - warp;
-    const int jend = kend > 0 ? (kend + kWarps - 1) / kWarps : 0;
+    const int jend = kend > 0 ? (kend + W - 1) / W : 0;
     float o[MT][4];
 #pragma unroll
     for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m = -INFINITY, M = -INFINITY, l = 0.f;   // of head g; l: this lane's share
+    // of heads 2t and 2t + 1; l: this lane's share
+    float m[2] = {kLowest, kLowest}, M[2] = {kLowest, kLowest}, l[2] = {0.f, 0.f};
 #pragma unroll 1
     for (; j < jend; ++j) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
       __syncwarp();
       const uint8_t* const st = ring + (j % kStages) * S::BYTES;
       const uint32_t vm = *reinterpret_cast<const uint32_t*>(st + S::MASK);
-      // logits: n-tile 0 = rows 0-7, n-tile 1 = rows 8-15
-      float sc[2][4];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-        const int r = nt * 8 + g;
-        const uint8_t* const krow = st + r * S::ROW;
-        const int sw = S::k_swz(r);
+      float* lg = nullptr;   // logits of head 2t, row g
+      if constexpr (ACC) lg = p.logits + ((size_t)u * G + 2 * t) * p.row_stride + (t0 + warp + j * W - seg_t0) * kTile + g;
+      if (vm) {
+        // x[2 r + e]: logit of row g + 8 r and head 2t + e
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint8_t* const k0 = st + g * S::ROW;   // rows g and g + 8 are swizzled alike
 #pragma unroll
         for (int i = 0; i < S::CH / 4; ++i) {
-          const uint4 w4 = *reinterpret_cast<const uint4*>(krow + (((4 * i + t) ^ sw) * 16));
-          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+          const int at = (S::k_chunk(i, t) ^ S::swz(g)) * 16;
+          const uint4 y0 = *reinterpret_cast<const uint4*>(k0 + at);
+          const uint4 y1 = *reinterpret_cast<const uint4*>(k0 + 8 * S::ROW + at);
+          const uint32_t w0[4] = {y0.x, y0.y, y0.z, y0.w}, w1[4] = {y1.x, y1.y, y1.z, y1.w};
           if constexpr (F::kEB == 1) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int ks = 4 * i + e;
-              const uint32_t x = CT::prep(w[e]);
-              const uint32_t b0 = CT::pair(x, 0), b1 = CT::pair(x, 1);
-              if constexpr (QP == 1) F::mma(sc[nt], qa[ks][0], 0u, qa[ks][1], 0u, b0, b1);
-              else F::mma(sc[nt], qa[ks][0], qa[ks][2], qa[ks][1], qa[ks][3], b0, b1);
+              const uint32_t z0 = CT::prep(w0[e]), z1 = CT::prep(w1[e]);
+              const uint32_t a0 = CT::pair(z0, 0), a1 = CT::pair(z1, 0), a2 = CT::pair(z0, 1), a3 = CT::pair(z1, 1);
+#pragma unroll
+              for (int part = 0; part < QP; ++part) F::mma(x, a0, a1, a2, a3, qa[ks][2 * part], qa[ks][2 * part + 1]);
             }
           } else {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int ks = 2 * i + e;
-              if constexpr (QP == 1) {
-                F::mma(sc[nt], qa[ks][0], 0u, qa[ks][1], 0u, w[2 * e], w[2 * e + 1]);
-              } else {
-                F::mma(sc[nt], qa[ks][0], qa[ks][2], qa[ks][1], qa[ks][3], w[2 * e], w[2 * e + 1]);
-                F::mma(sc[nt], qa[ks][4], 0u, qa[ks][5], 0u, w[2 * e], w[2 * e + 1]);
-              }
+#pragma unroll
+              for (int part = 0; part < QP; ++part)
+                F::mma(x, w0[2 * e], w1[2 * e], w0[2 * e + 1], w1[2 * e + 1], qa[ks][2 * part], qa[ks][2 * part + 1]);
             }
           }
         }
-      }
-      // softmax of head g over the lane's rows 2t, 2t+1, 8+2t, 9+2t
-      float x[4] = {sc[0][0], sc[0][1], sc[1][0], sc[1][1]};
-      if constexpr (QP > 1) {
-        x[0] += sc[0][2];
-        x[1] += sc[0][3];
-        x[2] += sc[1][2];
-        x[3] += sc[1][3];
-      }
-      int ve[4];
-      float vmant[4];
-      if constexpr (F::kScaled) {
-        const float2* const ksc = reinterpret_cast<const float2*>(st + S::SCALES);
-        const float2 k0 = ksc[t], k1 = ksc[4 + t], v0 = ksc[8 + t], v1 = ksc[12 + t];
-        x[0] *= k0.x * qfac;
-        x[1] *= k0.y * qfac;
-        x[2] *= k1.x * qfac;
-        x[3] *= k1.y * qfac;
-        const float vs[4] = {v0.x, v0.y, v1.x, v1.y};
+        float ve[2], vmant[2];   // V's scale of rows g and g + 8: 2^23 + its biased exponent, and its fraction
+        if constexpr (F::kScaled) {
+          const float* const ksc = reinterpret_cast<const float*>(st + S::SCALES);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t bits = __float_as_uint(vs[e]);
-          ve[e] = (int)(bits >> 23) - 127;
-          vmant[e] = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] *= qfac;
-      }
-      bool ok[4];
-      float mx = -INFINITY, Mx = -INFINITY;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        ok[e] = (vm >> (2 * t + (e & 1) + (e >> 1) * 8)) & 1u;
-        if (!ok[e]) x[e] = -INFINITY;
-        mx = fmaxf(mx, x[e]);
-        if constexpr (F::kScaled) Mx = fmaxf(Mx, x[e] + (float)ve[e]);
-      }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      if constexpr (F::kScaled) {
-        Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, 1));
-        Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, 2));
-      }
-      if constexpr (ACC) {
-        if (g < G) {
-          const int tl = t0 + warp + j * kWarps - seg_t0;   // tile of the unit
-          float* const lg = p.logits + ((size_t)u * G + g) * p.row_stride + tl * kTile + 2 * t;
-          *reinterpret_cast<float2*>(lg) = make_float2(x[0], x[1]);
-          *reinterpret_cast<float2*>(lg + 8) = make_float2(x[2], x[3]);
-        }
-      }
-      const float mn = fmaxf(m, ceilf(mx));
-      const float lcorr = mn == -INFINITY ? 1.f : ex2(m - mn);
-      float pr4[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) pr4[e] = ok[e] ? ex2(x[e] - mn) : 0.f;
-      l = l * lcorr + ((pr4[0] + pr4[1]) + (pr4[2] + pr4[3]));
-      m = mn;
-      float w4[4], ocorr;
-      if constexpr (F::kScaled) {
-        const float Mn = fmaxf(M, ceilf(Mx));
-        ocorr = Mn == -INFINITY ? 1.f : ex2(M - Mn);
-        M = Mn;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w4[e] = ok[e] ? ex2(x[e] + ((float)(ve[e] + kWBias) - Mn)) * vmant[e] : 0.f;
-      } else {
-        ocorr = lcorr;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w4[e] = pr4[e];
-      }
-      if (__any_sync(0xffffffffu, ocorr != 1.f)) {
-        const float c0 = __shfl_sync(0xffffffffu, ocorr, 8 * t), c1 = __shfl_sync(0xffffffffu, ocorr, 8 * t + 4);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          o[i][0] *= c0;
-          o[i][1] *= c1;
-          o[i][2] *= c0;
-          o[i][3] *= c1;
-        }
-      }
-      const uint32_t b0 = F::pack(w4[0], w4[1]), b1 = F::pack(w4[2], w4[3]);
-      uint32_t l0 = 0u, l1 = 0u;
-      if constexpr (WSPLIT) {
-        const float2 h0 = F::unpack(b0), h1 = F::unpack(b1);
-        l0 = F::pack(w4[0] - h0.x, w4[1] - h0.y);
-        l1 = F::pack(w4[2] - h1.x, w4[3] - h1.y);
-      }
-      // O^T += V^T . P: lane g holds a run of channels of the rows 2t, 2t+1, 8+2t, 9+2t
-      const uint8_t* const vb = st + S::HALF;
-      constexpr int CPG = D / 8;                       // channels per lane
-      constexpr int WPR = CPG * F::kEB / 4;            // words of them per row
-      uint32_t vw[4][WPR];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = 2 * t + (e & 1) + (e >> 1) * 8;
-        const uint8_t* const vrow = vb + r * S::ROW;
-        const int sw = S::v_swz(r);
-        if constexpr (WPR == 2) {
-          const uint2 y = *reinterpret_cast<const uint2*>(vrow + (((g >> 1) ^ sw) * 16) + (g & 1) * 8);
-          vw[e][0] = y.x;
-          vw[e][1] = y.y;
+          for (int r = 0; r < 2; ++r) {
+            const float k = ksc[8 * r + g];
+            x[2 * r] *= k * qfac[0];
+            x[2 * r + 1] *= k * qfac[1];
+            const uint32_t bits = __float_as_uint(ksc[16 + 8 * r + g]);
+            ve[r] = __uint_as_float((bits >> 23) | 0x4b000000u);
+            vmant[r] = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+          }
         } else {
 #pragma unroll
-          for (int c = 0; c < WPR / 4; ++c) {
-            const uint4 y = *reinterpret_cast<const uint4*>(vrow + (((WPR / 4 * g + c) ^ sw) * 16));
-            vw[e][4 * c] = y.x;
-            vw[e][4 * c + 1] = y.y;
-            vw[e][4 * c + 2] = y.z;
-            vw[e][4 * c + 3] = y.w;
+          for (int e = 0; e < 4; ++e) x[e] *= qfac[0];
+        }
+        if (vm != 0xffffu) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if (!((vm >> (g + 8 * r)) & 1u)) x[2 * r] = x[2 * r + 1] = -INFINITY;
+        }
+        if constexpr (ACC) {
+          if (2 * t < G) {
+            lg[0] = x[0];
+            lg[8] = x[2];
+          }
+          if (2 * t + 1 < G) {
+            lg[p.row_stride] = x[1];
+            lg[p.row_stride + 8] = x[3];
           }
         }
-      }
-      auto pv = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-        F::mma(o[i], a0, a1, a2, a3, b0, b1);
-        if constexpr (WSPLIT) F::mma(o[i], a0, a1, a2, a3, l0, l1);
-      };
+        // a: exponents of the weights, at most 14 where M holds; the maxima are raised only
+        // when a row of the tile passes them
+        float a[4];
+        const float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+        bool up = mx[0] > m[0] || mx[1] > m[1];
+        auto exponents = [&]() {
 #pragma unroll
-      for (int w = 0; w < WPR; ++w) {
-        if constexpr (F::kEB == 1) {   // 4 channels: m-tiles 2w and 2w + 1
-          const uint32_t e0 = CT::prep(__byte_perm(vw[0][w], vw[1][w], 0x5140));
-          const uint32_t e1 = CT::prep(__byte_perm(vw[0][w], vw[1][w], 0x7362));
-          const uint32_t f0 = CT::prep(__byte_perm(vw[2][w], vw[3][w], 0x5140));
-          const uint32_t f1 = CT::prep(__byte_perm(vw[2][w], vw[3][w], 0x7362));
-          pv(2 * w, CT::pair(e0, 0), CT::pair(e0, 1), CT::pair(f0, 0), CT::pair(f0, 1));
-          pv(2 * w + 1, CT::pair(e1, 0), CT::pair(e1, 1), CT::pair(f1, 0), CT::pair(f1, 1));
-        } else {                       // 2 channels: m-tile w
-          pv(w, __byte_perm(vw[0][w], vw[1][w], 0x5410), __byte_perm(vw[0][w], vw[1][w], 0x7632),
-             __byte_perm(vw[2][w], vw[3][w], 0x5410), __byte_perm(vw[2][w], vw[3][w], 0x7632));
+          for (int e = 0; e < 2; ++e) {
+            const float off = (float)kWBias - 8388735.f - M[e];   // integers below 2^24: exact
+            a[e] = x[e] + (ve[0] + off);
+            a[2 + e] = x[2 + e] + (ve[1] + off);
+          }
+        };
+        if constexpr (F::kScaled) {
+          exponents();
+          up |= fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) > (float)kWBias || M[0] == kLowest;
         }
+        if (__any_sync(0xffffffffu, up)) {
+          float corr[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mr = mx[e];
+            mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, 4));
+            mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, 8));
+            mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, 16));
+            const float mn = fmaxf(m[e], ceilf(mr));
+            corr[e] = ex2(m[e] - mn);
+            l[e] *= corr[e];
+            m[e] = mn;
+            if constexpr (F::kScaled) {
+              float Mr = fmaxf(x[e] + (ve[0] - 8388735.f), x[2 + e] + (ve[1] - 8388735.f));
+              Mr = fmaxf(Mr, __shfl_xor_sync(0xffffffffu, Mr, 4));
+              Mr = fmaxf(Mr, __shfl_xor_sync(0xffffffffu, Mr, 8));
+              Mr = fmaxf(Mr, __shfl_xor_sync(0xffffffffu, Mr, 16));
+              const float Mn = fmaxf(M[e], ceilf(Mr));
+              corr[e] = ex2(M[e] - Mn);
+              M[e] = Mn;
+            }
+          }
+          if constexpr (F::kScaled) exponents();
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            o[i][0] *= corr[0];
+            o[i][1] *= corr[1];
+            o[i][2] *= corr[0];
+            o[i][3] *= corr[1];
+          }
+        }
+        float w4[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w4[e] = ex2(x[e] - m[e & 1]);
+        l[0] += w4[0] + w4[2];
+        l[1] += w4[1] + w4[3];
+        if constexpr (F::kScaled) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w4[e] = ex2(a[e]) * vmant[e >> 1];
+        }
+        const uint32_t h0 = F::pack(w4[0], w4[1]), h1 = F::pack(w4[2], w4[3]);
+        const uint32_t b0 = movm(h0), b1 = movm(h1);   // rows 2t, 2t + 1 (+ 8) of head g
+        uint32_t l0 = 0u, l1 = 0u;
+        if constexpr (WSPLIT) {
+          const float2 f0 = F::unpack(h0), f1 = F::unpack(h1);
+          l0 = movm(F::pack(w4[0] - f0.x, w4[1] - f0.y));
+          l1 = movm(F::pack(w4[2] - f1.x, w4[3] - f1.y));
+        }
+        // O^T += V^T . P: lane g holds a run of channels of the rows 2t, 2t+1, 8+2t, 9+2t
+        const uint8_t* const vb = st + S::HALF;
+        constexpr int WPR = (D / 8) * F::kEB / 4;        // words of them per row
+        uint32_t vw[4][WPR];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 2 * t + (e & 1) + (e >> 1) * 8;
+          const uint8_t* const vrow = vb + r * S::ROW;
+          if constexpr (WPR == 2) {
+            const uint2 y = *reinterpret_cast<const uint2*>(vrow + (((g >> 1) ^ S::swz(r)) * 16) + (g & 1) * 8);
+            vw[e][0] = y.x;
+            vw[e][1] = y.y;
+          } else {
+#pragma unroll
+            for (int c = 0; c < WPR / 4; ++c) {
+              const uint4 y = *reinterpret_cast<const uint4*>(vrow + (((g + 8 * c) ^ S::swz(r)) * 16));
+              vw[e][4 * c] = y.x;
+              vw[e][4 * c + 1] = y.y;
+              vw[e][4 * c + 2] = y.z;
+              vw[e][4 * c + 3] = y.w;
+            }
+          }
+        }
+        auto pv = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+          F::mma(o[i], a0, a1, a2, a3, b0, b1);
+          if constexpr (WSPLIT) F::mma(o[i], a0, a1, a2, a3, l0, l1);
+        };
+#pragma unroll
+        for (int w = 0; w < WPR; ++w) {
+          if constexpr (F::kEB == 1) {   // 4 channels: m-tiles 2w and 2w + 1
+            const uint32_t e0 = CT::prep(__byte_perm(vw[0][w], vw[1][w], 0x5140));
+            const uint32_t e1 = CT::prep(__byte_perm(vw[0][w], vw[1][w], 0x7362));
+            const uint32_t f0 = CT::prep(__byte_perm(vw[2][w], vw[3][w], 0x5140));
+            const uint32_t f1 = CT::prep(__byte_perm(vw[2][w], vw[3][w], 0x7362));
+            pv(2 * w, CT::pair(e0, 0), CT::pair(e0, 1), CT::pair(f0, 0), CT::pair(f0, 1));
+            pv(2 * w + 1, CT::pair(e1, 0), CT::pair(e1, 1), CT::pair(f1, 0), CT::pair(f1, 1));
+          } else {                       // 2 channels: m-tile w
+            pv(w, __byte_perm(vw[0][w], vw[1][w], 0x5410), __byte_perm(vw[0][w], vw[1][w], 0x7632),
+               __byte_perm(vw[2][w], vw[3][w], 0x5410), __byte_perm(vw[2][w], vw[3][w], 0x7632));
+          }
+        }
+      } else if constexpr (ACC) {
+        if (2 * t < G) lg[0] = lg[8] = -INFINITY;
+        if (2 * t + 1 < G) lg[p.row_stride] = lg[p.row_stride + 8] = -INFINITY;
       }
       __syncwarp();
       issue();
-      fetch();
+      resolve();
+      request();
     }
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    if constexpr (!F::kScaled) M = m;
-
-    // ---- the warps' results of this unit meet in shared memory; position 16 i + 2 g + e of
-    // a head's row is channel (D / 8) g + 2 i + e
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      if (2 * t < G)
-        *reinterpret_cast<float2*>(mo + ((size_t)warp * G + 2 * t) * mo_stride(D) + 16 * i + 2 * g) =
-            make_float2(o[i][0], o[i][2]);
-      if (2 * t + 1 < G)
-        *reinterpret_cast<float2*>(mo + ((size_t)warp * G + 2 * t + 1) * mo_stride(D) + 16 * i + 2 * g) =
-            make_float2(o[i][1], o[i][3]);
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
+      if constexpr (!F::kScaled) M[e] = m[e];
     }
-    if (g < G && t == 0) {
-      float* const ml = mml + (warp * G + g) * 4;
-      ml[0] = m;
-      ml[1] = l;
-      ml[2] = M;
+
+    // ---- the warps' results of this unit meet in shared memory: the statistics first, then
+    // the outputs at a common scale, up to GM heads at a time; position 16 i + 2 g + e of a
+    // head's row is channel v_chan(i, g, e)
+    if (g == 0) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (2 * t + e < G)
+          *reinterpret_cast<float4*>(mml + (warp * G + 2 * t + e) * 4) = make_float4(m[e], l[e], M[e], 0.f);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (2 * t + e >= G) continue;
+      float MM = kLowest;
+#pragma unroll
+      for (int w = 0; w < W; ++w) MM = fmaxf(MM, mml[(w * G + 2 * t + e) * 4 + 2]);
+      const float f = ex2(M[e] - MM);   // a warp without rows: o = 0
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        o[i][e] *= f;
+        o[i][2 + e] *= f;
+      }
+    }
+    auto put = [&](int h0) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int hm = 2 * t + e - h0;
+        if (hm >= 0 && hm < GM) {
+          float* const row = mo + ((size_t)warp * GM + hm) * mo_stride(D) + 2 * g;
+#pragma unroll
+          for (int i = 0; i < MT; ++i) *reinterpret_cast<float2*>(row + 16 * i) = make_float2(o[i][e], o[i][2 + e]);
+        }
+      }
+    };
+    put(0);
+    if (threadIdx.x < G) {
+      float mm = kLowest, MM = kLowest, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        mm = fmaxf(mm, mml[(w * G + threadIdx.x) * 4]);
+        MM = fmaxf(MM, mml[(w * G + threadIdx.x) * 4 + 2]);
+      }
+#pragma unroll
+      for (int w = 0; w < W; ++w) L += mml[(w * G + threadIdx.x) * 4 + 1] * ex2(mml[(w * G + threadIdx.x) * 4] - mm);
+      s_unit[threadIdx.x] = make_float4(mm, L, MM, L == 0.f ? 0.f : ex2(MM - mm - (F::kScaled ? (float)kWBias : 0.f)) / L);
     }
     __syncthreads();
     const bool last = seg_end >= t1;
-    if (!last) load_q(u + 1);
     const bool starts = seg_t0 >= t0, ends = seg_t0 + un <= t1;
     const bool alone = starts && ends;
     const int slot = 2 * cta + (u == u0 ? 0 : 1);
     if (!p.whole && starts && threadIdx.x == 0)
       p.info[u] = make_int4(cta, ends ? cta : range_owner(seg_t0 + un - 1, total, N), slot, 0);
     const int b = u / p.n_kv, h = u - b * p.n_kv;
-    for (int e = threadIdx.x; e < G * D; e += kThreads) {
-      const int gg = e / D, pos = e - gg * D;
-      const int c = (D / 8) * ((pos & 15) >> 1) + 2 * (pos >> 4) + (pos & 1);
-      float mm = -INFINITY, MM = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        mm = fmaxf(mm, mml[(w * G + gg) * 4]);
-        MM = fmaxf(MM, mml[(w * G + gg) * 4 + 2]);
+    for (int h0 = 0; h0 < G; h0 += GM) {
+      if (h0) {
+        __syncthreads();
+        put(h0);
+        __syncthreads();
       }
-      float L = 0.f, O = 0.f;
-      if (mm != -INFINITY) {
+      for (int e = threadIdx.x; e < GM * D; e += THREADS) {
+        const int hm = e / D, pos = e - hm * D, gg = h0 + hm;
+        const int c = S::v_chan(pos >> 4, (pos & 15) >> 1, pos & 1);
+        float O = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float* const ml = mml + (w * G + gg) * 4;
-          if (ml[0] == -INFINITY) continue;
-          L += ml[1] * ex2(ml[0] - mm);
-          O += mo[((size_t)w * G + gg) * mo_stride(D) + pos] * ex2(ml[2] - MM);
-        }
-      }
-      const size_t bh = (size_t)b * p.n_q_heads + h * G + gg;
-      if (alone) {
-        const float scale = F::kScaled ? ex2(MM - mm - (float)kWBias) : 1.f;
-        const float y = mm == -INFINITY ? 0.f : O / L * scale;
-        if (p.out_f32) static_cast<float*>(p.out)[bh * D + c] = y;
-        else static_cast<__nv_bfloat16*>(p.out)[bh * D + c] = __float2bfloat16_rn(y);
-        if (pos == 0) {
-          if (p.lse) p.lse[bh] = mm == -INFINITY ? -INFINITY : mm * kLn2 + logf(L);
-          if constexpr (ACC) {
-            p.stat[((size_t)u * G + gg) * 2] = mm;
-            p.stat[((size_t)u * G + gg) * 2 + 1] = mm == -INFINITY ? 0.f : 1.f / L;
+        for (int w = 0; w < W; ++w) O += mo[((size_t)w * GM + hm) * mo_stride(D) + pos];
+        const float4 un4 = s_unit[gg];
+        const size_t bh = (size_t)b * p.n_q_heads + h * G + gg;
+        if (alone) {
+          const float y = un4.y == 0.f ? 0.f : O * un4.w;
+          if (p.out_f32) static_cast<float*>(p.out)[bh * D + c] = y;
+          else static_cast<__nv_bfloat16*>(p.out)[bh * D + c] = __float2bfloat16_rn(y);
+          if (pos == 0) {
+            if (p.lse) p.lse[bh] = un4.y == 0.f ? -INFINITY : un4.x * kLn2 + logf(un4.y);
+            if constexpr (ACC) {
+              p.stat[((size_t)u * G + gg) * 2] = un4.x;
+              p.stat[((size_t)u * G + gg) * 2 + 1] = un4.y == 0.f ? 0.f : 1.f / un4.y;
+            }
           }
-        }
-      } else {
-        p.part_o[((size_t)slot * G + gg) * D + c] = O;
-        if (pos == 0) {
-          float* const ml = p.part_ml + ((size_t)slot * G + gg) * 4;
-          ml[0] = mm;
-          ml[1] = L;
-          ml[2] = MM;
+        } else {
+          p.part_o[((size_t)slot * G + gg) * D + c] = O;
+          if (pos == 0) *reinterpret_cast<float4*>(p.part_ml + ((size_t)slot * G + gg) * 4) = un4;
         }
       }
     }
     if constexpr (ACC) {
       if (p.whole) {   // this CTA holds every logit of the unit: the weights right away
         __syncthreads();
-        for (int r = threadIdx.x; r < ur.n_rows; r += kThreads) {
-          float w = 0.f;
-          bool any = false;
-          for (int gg = 0; gg < G; ++gg) {
-            const float xv = p.logits[((size_t)u * G + gg) * p.row_stride + r];
-            if (xv == -INFINITY) continue;
-            any = true;
-            w += ex2(xv - p.stat[((size_t)u * G + gg) * 2]) * p.stat[((size_t)u * G + gg) * 2 + 1];
-          }
-          if (!any) continue;
-          const int tok = r < ur.n_sel ? p.idx[(size_t)u * p.C + r] : ur.tb + (r - ur.n_sel);
-          atomicAdd(p.acc + (size_t)u * p.t_max + tok, w);
-        }
+        const float* const stat = p.stat + (size_t)u * G * 2;
+        for (int r = threadIdx.x; r < ur.n_rows; r += THREADS)
+          add_weights<1>(p, u, ur, r, ur.n_rows, [&](int gg, float xv) { return ex2(xv - stat[2 * gg]) * stat[2 * gg + 1]; });
       }
     }
     if (last) break;
-    __syncthreads();
+    load_q(u + 1);
+    // no barrier here: mml was read before the last one, and mo and s_unit are written again
+    // after the next unit's first
     seg_t0 += un;
   }
 }
 
 // Joins the units that several CTAs share (one CTA per unit) and, for ACC, adds the weights
 // of the unit's rows (blockIdx.y: chunks of kAccRows rows).
-constexpr int kAccRows = 1024;
-
 template <int D, bool ACC>
-__global__ void __launch_bounds__(kThreads) finish_kernel(FlatParams p, float bias) {
-  __shared__ float s_m[8], s_il[8];
-  const int u = blockIdx.x, G = p.G;
+__global__ void __launch_bounds__(kFinThreads) finish_kernel(FlatParams p, float bias) {
+  __shared__ float fac[8][kMaxCtas];       // weight of a CTA's output
+  __shared__ float s_m[8], s_l[8], s_M[8];
+  __shared__ float4 red[kFinThreads];
+  const int u = blockIdx.x, G = p.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   const int4 in = p.info[u];
-  const int n = in.y - in.x + 1;   // CTAs of the unit
-  auto slot_of = [&](int i) -> int { return i == 0 ? in.z : 2 * (in.x + i); };
-  const bool shared = n > 1;
-  if (ACC && blockIdx.y * kAccRows >= p.row_stride) return;
+  const int n = in.y - in.x + 1;           // CTAs of the unit
+  const bool join = n > 1 && blockIdx.y == 0;
+  if (!ACC && !join) return;
   UnitRows ur;
   if constexpr (ACC) {
     ur = unit_rows(p, u, false);
-    if (blockIdx.y > 0 && (int)blockIdx.y * kAccRows >= ur.n_rows) return;
+    if (!join && (int)blockIdx.y * kAccRows >= ur.n_rows) return;
   }
-  if (shared && blockIdx.y == 0) {
-    const int b = u / p.n_kv, h = u - b * p.n_kv;
-    for (int e = threadIdx.x; e < G * D; e += kThreads) {
-      const int gg = e / D, c = e - gg * D;
-      float mm = -INFINITY, MM = -INFINITY;
-      for (int i = 0; i < n; ++i) {
-        const float* const ml = p.part_ml + ((size_t)slot_of(i) * G + gg) * 4;
-        mm = fmaxf(mm, ml[0]);
-        MM = fmaxf(MM, ml[2]);
+  auto slot_of = [&](int i) -> int { return i == 0 ? in.z : 2 * (in.x + i); };
+  if (warp < G) {   // warp gg: statistics of head gg
+    if (n > 1) {
+      float mm = kLowest, MM = kLowest, L = 0.f;
+      for (int i = lane; i < n; i += 32) {
+        const float4 ml = *reinterpret_cast<const float4*>(p.part_ml + ((size_t)slot_of(i) * G + warp) * 4);
+        fac[warp][i] = ml.z;
+        MM = fmaxf(MM, ml.z);
+        const float mn = fmaxf(mm, ml.x);
+        L = L * ex2(mm - mn) + ml.y * ex2(ml.x - mn);
+        mm = mn;
       }
-      float L = 0.f, O = 0.f;
-      if (mm != -INFINITY) {
-        for (int i = 0; i < n; ++i) {
-          const float* const ml = p.part_ml + ((size_t)slot_of(i) * G + gg) * 4;
-          if (ml[0] == -INFINITY) continue;
-          L += ml[1] * ex2(ml[0] - mm);
-          O += p.part_o[((size_t)slot_of(i) * G + gg) * D + c] * ex2(ml[2] - MM);
-        }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        MM = fmaxf(MM, __shfl_xor_sync(0xffffffffu, MM, o));
+        const float m2 = __shfl_xor_sync(0xffffffffu, mm, o), l2 = __shfl_xor_sync(0xffffffffu, L, o);
+        const float mn = fmaxf(mm, m2);
+        L = L * ex2(mm - mn) + l2 * ex2(m2 - mn);
+        mm = mn;
       }
+      for (int i = lane; i < n; i += 32) fac[warp][i] = ex2(fac[warp][i] - MM);
+      if (lane == 0) {
+        s_m[warp] = mm;
+        s_l[warp] = L;
+        s_M[warp] = MM;
+      }
+    } else if (lane == 0) {
+      s_m[warp] = p.stat[((size_t)u * G + warp) * 2];
+      s_l[warp] = p.stat[((size_t)u * G + warp) * 2 + 1];   // 1 / l
+    }
+  }
+  __syncthreads();
+  if (join) {   // four channels per thread; groups of threads take every ngrp-th CTA's output
+    const int cols = G * D / 4, ngrp = kFinThreads / cols;
+    const int col = threadIdx.x % cols, grp = threadIdx.x / cols;
+    const int gg = 4 * col / D, c = 4 * col - gg * D;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = grp; i < n; i += ngrp) {
+      const float4 x = *reinterpret_cast<const float4*>(p.part_o + ((size_t)slot_of(i) * G + gg) * D + c);
+      const float f = fac[gg][i];
+      a.x += x.x * f;
+      a.y += x.y * f;
+      a.z += x.z * f;
+      a.w += x.w * f;
+    }
+    red[threadIdx.x] = a;
+    __syncthreads();
+    if (grp == 0) {
+      for (int k = 1; k < ngrp; ++k) {
+        const float4 x = red[k * cols + col];
+        a.x += x.x;
+        a.y += x.y;
+        a.z += x.z;
+        a.w += x.w;
+      }
+      const int b = u / p.n_kv, h = u - b * p.n_kv;
       const size_t bh = (size_t)b * p.n_q_heads + h * G + gg;
-      const float y = mm == -INFINITY ? 0.f : O / L * ex2(MM - mm - bias);
-      if (p.out_f32) static_cast<float*>(p.out)[bh * D + c] = y;
-      else static_cast<__nv_bfloat16*>(p.out)[bh * D + c] = __float2bfloat16_rn(y);
-      if (c == 0 && p.lse) p.lse[bh] = mm == -INFINITY ? -INFINITY : mm * kLn2 + logf(L);
+      const float L = s_l[gg], mm = s_m[gg];
+      const float f = ex2(s_M[gg] - mm - bias);
+      const float y[4] = {a.x / L * f, a.y / L * f, a.z / L * f, a.w / L * f};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float v = L == 0.f ? 0.f : y[e];
+        if (p.out_f32) static_cast<float*>(p.out)[bh * D + c + e] = v;
+        else static_cast<__nv_bfloat16*>(p.out)[bh * D + c + e] = __float2bfloat16_rn(v);
+      }
+      if (c == 0 && p.lse) p.lse[bh] = L == 0.f ? -INFINITY : mm * kLn2 + logf(L);
     }
   }
   if constexpr (ACC) {
-    if (threadIdx.x < G) {
-      const int gg = threadIdx.x;
-      float mm = -INFINITY, L = 0.f;
-      if (shared) {
-        for (int i = 0; i < n; ++i) mm = fmaxf(mm, p.part_ml[((size_t)slot_of(i) * G + gg) * 4]);
-        if (mm != -INFINITY)
-          for (int i = 0; i < n; ++i) {
-            const float* const ml = p.part_ml + ((size_t)slot_of(i) * G + gg) * 4;
-            if (ml[0] != -INFINITY) L += ml[1] * ex2(ml[0] - mm);
-          }
-        s_m[gg] = mm;
-        s_il[gg] = mm == -INFINITY ? 0.f : 1.f / L;
-      } else {
-        s_m[gg] = p.stat[((size_t)u * G + gg) * 2];
-        s_il[gg] = p.stat[((size_t)u * G + gg) * 2 + 1];
-      }
-    }
+    __syncthreads();
+    if (n > 1 && threadIdx.x < G) s_l[threadIdx.x] = s_l[threadIdx.x] == 0.f ? 0.f : 1.f / s_l[threadIdx.x];
     __syncthreads();
     const int r1 = min(ur.n_rows, ((int)blockIdx.y + 1) * kAccRows);
-    for (int r = blockIdx.y * kAccRows + threadIdx.x; r < r1; r += kThreads) {
-      float w = 0.f;
-      bool any = false;
-      for (int gg = 0; gg < G; ++gg) {
-        const float xv = p.logits[((size_t)u * G + gg) * p.row_stride + r];
-        if (xv == -INFINITY) continue;   // a row that was not attended
-        any = true;
-        w += ex2(xv - s_m[gg]) * s_il[gg];
-      }
-      if (!any) continue;
-      const int tok = r < ur.n_sel ? p.idx[(size_t)u * p.C + r] : ur.tb + (r - ur.n_sel);
-      atomicAdd(p.acc + (size_t)u * p.t_max + tok, w);
-    }
+    add_weights<kAccVecs>(p, u, ur, blockIdx.y * kAccRows + threadIdx.x, r1,
+                [&](int gg, float xv) { return ex2(xv - s_m[gg]) * s_l[gg]; });
   }
 }
 
 // acc from the logits (base 2) of attend_kernel and the final lse.
-__global__ void __launch_bounds__(kThreads) accumulate_kernel(FlatParams p) {
+__global__ void __launch_bounds__(kFinThreads) accumulate_kernel(FlatParams p) {
   __shared__ float s_l[8];
   const int u = blockIdx.x, G = p.G;
   const int b = u / p.n_kv, h = u - b * p.n_kv;
@@ -747,29 +913,18 @@ __global__ void __launch_bounds__(kThreads) accumulate_kernel(FlatParams p) {
   if (threadIdx.x < G) s_l[threadIdx.x] = p.lse[(size_t)b * p.n_q_heads + h * G + threadIdx.x];
   __syncthreads();
   const int r1 = min(ur.n_rows, ((int)blockIdx.y + 1) * kAccRows);
-  for (int r = blockIdx.y * kAccRows + threadIdx.x; r < r1; r += kThreads) {
-    float w = 0.f;
-    bool any = false;
-    for (int gg = 0; gg < G; ++gg) {
-      const float xv = p.logits[((size_t)u * G + gg) * p.row_stride + r];
-      if (xv == -INFINITY) continue;
-      any = true;
-      w += expf(xv * kLn2 - s_l[gg]);
-    }
-    if (!any) continue;
-    const int tok = r < ur.n_sel ? p.idx[(size_t)u * p.C + r] : ur.tb + (r - ur.n_sel);
-    atomicAdd(p.acc + (size_t)u * p.t_max + tok, w);
-  }
+  add_weights<kAccVecs>(p, u, ur, blockIdx.y * kAccRows + threadIdx.x, r1,
+              [&](int gg, float xv) { return expf(xv * kLn2 - s_l[gg]); });
 }
 
 template <typename CT, int D, int QP, bool ACC>
 cudaError_t launch_flat_t(const FlatParams& p, int ctas, int chunks, cudaStream_t s) {
   auto kern = attend_flat_kernel<CT, D, QP, ACC>;
   const size_t smem = flat_smem<CT, D>(p.G);
-  if (prepare_kernel((const void*)kern, smem, kThreads) < 1) return cudaErrorInvalidConfiguration;
-  cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, s, p);
+  if (prepare_kernel((const void*)kern, smem, Fmt<CT>::kWarps * 32) < 1) return cudaErrorInvalidConfiguration;
+  cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(Fmt<CT>::kWarps * 32), smem, s, p);
   if (e != cudaSuccess || p.whole) return e;
-  return launch_pdl(finish_kernel<D, ACC>, dim3(p.units, ACC ? chunks : 1), dim3(kThreads), 0, s, p,
+  return launch_pdl(finish_kernel<D, ACC>, dim3(p.units, ACC ? chunks : 1), dim3(kFinThreads), 0, s, p,
                     Fmt<CT>::kScaled ? (float)kWBias : 0.f);
 }
 
@@ -790,6 +945,7 @@ FlatParams flat_params(const void* q, int q_f32, int n_q_heads, const KvView& kv
   FlatParams p = {};
   p.q = q;
   p.q_f32 = q_f32;
+  p.q_aligned = (reinterpret_cast<uintptr_t>(q) & 15) == 0;
   p.n_q_heads = n_q_heads;
   p.G = n_q_heads / kv.n_kv;
   p.k = static_cast<const uint8_t*>(kv.k);
@@ -804,6 +960,8 @@ FlatParams flat_params(const void* q, int q_f32, int n_q_heads, const KvView& kv
   p.page_size = kv.page_size;
   p.max_pages = kv.max_pages;
   p.n_pages = kv.n_pages;
+  const int m16 = kv.page_size / 16;
+  p.page_magic = m16 > 1 ? (uint32_t)(((1ull << 32) + m16 - 1) / m16) : 0u;
   p.page_table = kv.page_table;
   p.seq_lens = kv.seq_lens;
   p.idx = idx;
@@ -819,9 +977,10 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-// A unit of at most kWholeRows rows stays whole: joining costs a second launch.
-constexpr int kWholeRows = 256;
-constexpr int kFlatSms = 148;
+// A unit of at most kWholeRows rows stays whole: four tiles per warp cost less than joining
+// the shares of several CTAs in a second launch (2 units of 512 rows, fp32 query: 11.2 us
+// shared).
+constexpr int kWholeRows = 512;
 
 FlatPlan flat_plan(int batch, int n_q_heads, int n_kv_heads, int head_dim, int C, int max_tail, bool kv8,
                    bool accumulate, int ctas_per_sm) {
@@ -830,8 +989,9 @@ FlatPlan flat_plan(int batch, int n_q_heads, int n_kv_heads, int head_dim, int C
   const long units = (long)batch * n_kv_heads;
   const int G = n_q_heads / n_kv_heads;
   const long tiles = units * ((rows + kTile - 1) / kTile);
-  long ctas = (tiles + kWarps - 1) / kWarps;
-  const long most = (long)kFlatSms * (ctas_per_sm > 0 ? ctas_per_sm : (kv8 ? 2 : 1));
+  const long ctas = (tiles + kMinTiles - 1) / kMinTiles;
+  // the decode step leaves room beside the attention for the key scan: one CTA per SM
+  const long most = (long)kFlatSms * (ctas_per_sm > 0 ? ctas_per_sm : (kv8 ? Fmt<CodeE4M3>::kCtas : 1));
   pl.whole = rows <= kWholeRows ? 1 : 0;
   pl.ctas = (int)(pl.whole ? units : (ctas < most ? (ctas < 1 ? 1 : ctas) : most));
   pl.row_stride = accumulate ? (int)((rows + kTile - 1) / kTile * kTile) : 0;
@@ -881,7 +1041,7 @@ cudaError_t launch_accumulate(const float* logits, int row_stride, const float* 
   p.row_stride = row_stride;
   p.lse = const_cast<float*>(lse);
   p.acc = acc;
-  return launch_pdl(accumulate_kernel, dim3(p.units, (row_stride + kAccRows - 1) / kAccRows), dim3(kThreads), 0, s, p);
+  return launch_pdl(accumulate_kernel, dim3(p.units, (row_stride + kAccRows - 1) / kAccRows), dim3(kFinThreads), 0, s, p);
 }
 
 ASP_STATUS_READER(read_status_attend_flat)

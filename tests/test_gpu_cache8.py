@@ -423,7 +423,7 @@ def test_attend_accumulate(fmt, qd, d, G, page, C, tail):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "bf16", "f32"])
-@pytest.mark.parametrize("T", [1, 16, 250, 256, 257])
+@pytest.mark.parametrize("T", [1, 16, 250, 256, 257, 512, 513])
 def test_short_caches(fmt, T):
     c = Cache(fmt, 2, 2, 128, T, [T, max(0, T - 1)], 0, 16, seed=T)
     q = torch.randn(2, 8, 128, generator=gen(5)).to(torch.bfloat16).to(DEV)
