@@ -16,6 +16,11 @@ struct Vec;   // 16 bytes of source values as fp32
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
+  // running maximum of |x| as bits, infinities and NaN included; top() of it as fp32 bits
+  __device__ __forceinline__ static void amax(uint32_t& m, const uint4& u) {
+    m = max(max(m, max(u.x & 0x7fffffffu, u.y & 0x7fffffffu)), max(u.z & 0x7fffffffu, u.w & 0x7fffffffu));
+  }
+  __device__ __forceinline__ static uint32_t top(uint32_t m) { return m; }
   __device__ __forceinline__ static void get(const uint4& u, float (&x)[4]) {
     x[0] = __uint_as_float(u.x);
     x[1] = __uint_as_float(u.y);
@@ -26,6 +31,11 @@ struct Vec<float> {
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
+  __device__ __forceinline__ static void amax(uint32_t& m, const uint4& u) {   // two 16-bit maxima
+    m = __vmaxu2(__vmaxu2(m, __vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu)),
+                 __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+  }
+  __device__ __forceinline__ static uint32_t top(uint32_t m) { return max(m << 16, m & 0xffff0000u); }
   __device__ __forceinline__ static void get(const uint4& u, float (&x)[8]) {
     float2 f[4];
     Elem<__nv_bfloat16>::unpack(u, f);
@@ -38,74 +48,123 @@ struct Vec<__nv_bfloat16> {
 };
 
 // A scale block stays in the registers of TPB threads between its maximum and its codes:
-// one pass over the source.  Blocks of up to 16 KB keep 4 vectors per thread in flight
-// (larger ones 8 or 16), a CTA holds 256 / TPB blocks.  Neighbouring blocks are those of
-// the next KV head, so that a [batch, token, head, channel] source, whose rows of one head
-// lie apart, is still read in whole runs.
+// one pass over the source.  A thread keeps 8 vectors (2 KB blocks 4, 64 KB blocks 16), a CTA
+// holds 256 / TPB blocks.  The grid is resident and a CTA requests its next block before it
+// encodes the present one (but for 64 KB blocks, whose registers are full).
+// Neighbouring CTAs take neighbouring KV heads, so that a [batch, token, head, channel]
+// source, whose rows of one head lie apart, is still read in whole runs.
 template <typename ST, typename CT, int D, int BL>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(KvView kv, const ST* __restrict__ k_src,
+struct QuantLayout {
+  static constexpr int N = Vec<ST>::N;
+  static constexpr int VPR = D / N;                 // vectors of a row
+  static constexpr int VB = BL * VPR;               // vectors of a block
+  static constexpr int NV = VB < 256 ? 4 : (VB <= 8 * kThreads ? 8 : 16);
+  static constexpr int TPB = VB / NV;               // threads of a block: 32 to 256
+  static constexpr int BPC = kThreads / TPB;        // blocks of a CTA
+  static constexpr bool AHEAD = NV <= 8;
+  static constexpr int CTAS = NV > 4 ? 2 : 3;       // per SM
+  static_assert(TPB >= 32 && TPB <= kThreads && TPB * NV == VB, "layout");
+};
+
+template <typename ST, typename CT, int D, int BL>
+__global__ void __launch_bounds__(kThreads, QuantLayout<ST, CT, D, BL>::CTAS) quantize_kernel(KvView kv, const ST* __restrict__ k_src,
                                                             const ST* __restrict__ v_src, Strides3 st, int nb,
                                                             long long items) {
-  constexpr int N = Vec<ST>::N;
-  constexpr int VPR = D / N;                 // vectors of a row
-  constexpr int VB = BL * VPR;               // vectors of a block
-  constexpr int NV = VB <= 4 * kThreads ? 4 : VB / kThreads;
-  constexpr int TPB = VB / NV;               // threads of a block: 32 to 256
-  constexpr int BPC = kThreads / TPB;        // blocks of a CTA
-  static_assert(TPB >= 32 && TPB <= kThreads && TPB * NV == VB, "layout");
+  using L = QuantLayout<ST, CT, D, BL>;
+  constexpr int N = L::N, VPR = L::VPR, NV = L::NV, TPB = L::TPB;
   __shared__ uint32_t wmax[2][kThreads / 32];
   const int sub = threadIdx.x / TPB, t = threadIdx.x % TPB, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const ST* const src = blockIdx.y ? v_src : k_src;
   uint8_t* const code = static_cast<uint8_t*>(const_cast<void*>(blockIdx.y ? kv.v : kv.k));
   float* const scale = blockIdx.y ? kv.v_scale : kv.k_scale;
-  const int stride = gridDim.x * BPC;
-  int turn = 0;
-  for (long long base = (long long)blockIdx.x * BPC; base < items; base += stride, turn ^= 1) {
-    const long long item = base + sub;
-    const int h = (int)(item % kv.n_kv);
-    const long long bi = item / kv.n_kv;
-    const int i = (int)(bi % nb), b = (int)(bi / nb);
-    int T = 0;
+  const long long stride = (long long)gridDim.x * L::BPC;
+  // the thread's item as (sequence, block, head), moved on by the stride without divisions
+  long long item = (long long)blockIdx.x * L::BPC + sub;
+  int h = (int)(item % kv.n_kv), i = (int)(item / kv.n_kv % nb);
+  long long b = item / kv.n_kv / nb;
+  const int dh = (int)(stride % kv.n_kv), di = (int)(stride / kv.n_kv % nb);
+  const long long db = stride / kv.n_kv / nb;
+
+  struct Block {
+    int rows;            // rows of the block that hold tokens (0: nothing to do)
+    size_t row0, sidx;
+    uint4 u[NV];
+  };
+  auto load = [&](Block& q) {
+    q.rows = 0;
     if (item < items) {
-      T = kv.seq_lens ? kv.seq_lens[b] : kv.t_max;
+      int T = kv.seq_lens ? kv.seq_lens[b] : kv.t_max;
       T = T > kv.t_max ? kv.t_max : T;
-    }
-    const int tok0 = i * BL;
-    bool live = tok0 < T;
-    size_t row0 = 0, sidx = 0;
-    if (live) {
-      if (kv.page_size == 0) {
-        row0 = ((size_t)b * kv.n_kv + h) * kv.t_max + tok0;
-        sidx = ((size_t)b * kv.n_kv + h) * kv.blocks_per_row + i;
-      } else {   // a block lies within one page
-        const int page = kv.page_table[(size_t)b * kv.max_pages + tok0 / kv.page_size];
-        if (page < 0 || page >= kv.n_pages) {
-          if (t == 0) flag_status(ASP_DEV_BAD_PAGE);
-          live = false;
-        } else {
-          const int r = tok0 % kv.page_size;
-          row0 = ((size_t)page * kv.n_kv + h) * kv.page_size + r;
-          sidx = ((size_t)page * kv.n_kv + h) * kv.blocks_per_row + r / BL;
+      const int tok0 = i * BL;
+      q.rows = T - tok0 > BL ? BL : (T > tok0 ? T - tok0 : 0);
+      if (q.rows) {
+        if (kv.page_size == 0) {
+          q.row0 = ((size_t)b * kv.n_kv + h) * kv.t_max + tok0;
+          q.sidx = ((size_t)b * kv.n_kv + h) * kv.blocks_per_row + i;
+        } else {   // a block lies within one page
+          const int page = kv.page_table[(size_t)b * kv.max_pages + tok0 / kv.page_size];
+          if (page < 0 || page >= kv.n_pages) {
+            if (t == 0) flag_status(ASP_DEV_BAD_PAGE);
+            q.rows = 0;
+          } else {
+            const int r = tok0 % kv.page_size;
+            q.row0 = ((size_t)page * kv.n_kv + h) * kv.page_size + r;
+            q.sidx = ((size_t)page * kv.n_kv + h) * kv.blocks_per_row + r / BL;
+          }
         }
       }
-    }
-    uint4 u[NV];
-    const ST* const s0 = src + (size_t)b * st.batch + (size_t)h * st.head;
+      const ST* const s0 = src + (size_t)b * st.batch + (size_t)h * st.head + (size_t)tok0 * st.token;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int vec = v * TPB + t, r = vec / VPR;
-      u[v] = live && tok0 + r < T
-                 ? *reinterpret_cast<const uint4*>(s0 + (size_t)(tok0 + r) * st.token + (vec % VPR) * N)
-                 : make_uint4(0u, 0u, 0u, 0u);
+      for (int v = 0; v < NV; ++v) {
+        const int vec = v * TPB + t, r = vec / VPR;
+        q.u[v] = r < q.rows ? *reinterpret_cast<const uint4*>(s0 + (size_t)r * st.token + (vec % VPR) * N)
+                            : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    item += stride;
+    h += dh;
+    i += di;
+    b += db;
+    if (h >= kv.n_kv) {
+      h -= kv.n_kv;
+      ++i;
+    }
+    if (i >= nb) {
+      i -= nb;
+      ++b;
+    }
+  };
+
+  Block cur, nxt;
+  if (L::AHEAD) load(nxt);
+  int turn = 0;
+  for (long long base = (long long)blockIdx.x * L::BPC; base < items; base += stride, turn ^= 1) {
+    if constexpr (L::AHEAD) {
+      cur = nxt;
+      load(nxt);
+    } else {
+      load(cur);
     }
     uint32_t amax = 0u;
     bool bad = false;
+    if (cur.rows) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      float x[N];
-      Vec<ST>::get(u[v], x);
+      for (int v = 0; v < NV; ++v) Vec<ST>::amax(amax, cur.u[v]);
+      amax = Vec<ST>::top(amax);
+      if (amax >= 0x7f800000u) {   // an infinity or NaN among them: the finite ones again
+        amax = 0u;
+#pragma unroll 1
+        for (int v = 0; v < NV; ++v) {
+          uint4 u = cur.u[0];
 #pragma unroll
-      for (int e = 0; e < N; ++e) amax = max(amax, finite_abs(x[e], bad));
+          for (int k = 1; k < NV; ++k)
+            if (k == v) u = cur.u[k];
+          float x[N];
+          Vec<ST>::get(u, x);
+#pragma unroll
+          for (int e = 0; e < N; ++e) amax = max(amax, finite_abs(x[e], bad));
+        }
+      }
     }
     amax = __reduce_max_sync(0xffffffffu, amax);
     if constexpr (TPB > 32) {   // two alternating arrays: one barrier per block
@@ -114,46 +173,55 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(KvView kv, const ST*
 #pragma unroll
       for (int w = 0; w < TPB / 32; ++w) amax = max(amax, wmax[turn][sub * (TPB / 32) + w]);
     }
-    if (!live) continue;
+    if (!cur.rows) continue;
     if (bad) flag_status(ASP_DEV_NONFINITE);
     const int e = scale_exp<CT>(amax);
     const float inv = exp2i(-e);
-    if (t == 0) scale[sidx] = exp2i(e);
+    if (t == 0) scale[cur.sidx] = exp2i(e);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int vec = v * TPB + t, r = vec / VPR;
-      if (tok0 + r >= T) continue;
+      if (r >= cur.rows) continue;
       float x[N];
-      Vec<ST>::get(u[v], x);
+      Vec<ST>::get(cur.u[v], x);
       uint32_t w[N / 4];
 #pragma unroll
       for (int j = 0; j < N / 4; ++j)
         w[j] = CT::encode4(x[4 * j] * inv, x[4 * j + 1] * inv, x[4 * j + 2] * inv, x[4 * j + 3] * inv);
-      uint8_t* const dst = code + (row0 + r) * D + (vec % VPR) * N;
+      uint8_t* const dst = code + (cur.row0 + r) * D + (vec % VPR) * N;
       if constexpr (N == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
       else *reinterpret_cast<uint32_t*>(dst) = w[0];
     }
   }
 }
 
-// Four vectors of 16 codes per thread and turn, in the cache's row order.
-template <typename DT, typename CT, int D>
+// UV (2 or 8) vectors of 8 codes (bf16 values) or 4 (fp32) per thread and turn, in the cache's row
+// order: a warp's 16-byte stores of one turn follow one another.  (16 codes per thread, whose
+// two stores leave gaps of 16 bytes: 280 us for 2 x 268 M codes into bf16.)
+template <typename DT, int D, int UV>
+struct DeqLayout {
+  static constexpr int N = 16 / (int)sizeof(DT);   // codes per vector
+  static constexpr int VPR = D / N;
+  static constexpr int U = UV;
+  static constexpr int ROWS = U * kThreads / VPR;  // tokens of a tile
+};
+
+template <typename DT, typename CT, int D, int UV>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(KvView kv, DT* __restrict__ k_dst,
                                                               DT* __restrict__ v_dst, Strides3 st, int tiles) {
-  constexpr int VPR = D / 16;
-  constexpr int U = 4;
-  constexpr int ROWS = U * kThreads / VPR;   // tokens of a tile
-  const uint8_t* const code = static_cast<const uint8_t*>(blockIdx.y ? kv.v : kv.k);
-  const float* const scale = blockIdx.y ? kv.v_scale : kv.k_scale;
-  DT* const dst = blockIdx.y ? v_dst : k_dst;
-  const long long items = (long long)kv.batch * kv.n_kv * tiles;
-  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
-    const int unit = (int)(item / tiles), tile = (int)(item - (long long)unit * tiles);
+  using L = DeqLayout<DT, D, UV>;
+  constexpr int N = L::N, VPR = L::VPR, U = L::U, ROWS = L::ROWS;
+  const uint8_t* const code = static_cast<const uint8_t*>(blockIdx.z ? kv.v : kv.k);
+  const float* const scale = blockIdx.z ? kv.v_scale : kv.k_scale;
+  DT* const dst = blockIdx.z ? v_dst : k_dst;
+  // the units' first tiles come first: the CTAs past short sequences end the launch
+  const int unit = blockIdx.x;
+  for (int tile = blockIdx.y; tile < tiles; tile += gridDim.y) {
     const int b = unit / kv.n_kv, h = unit - b * kv.n_kv;
     int T = kv.seq_lens ? kv.seq_lens[b] : kv.t_max;
     T = T > kv.t_max ? kv.t_max : T;
     if (tile * ROWS >= T) continue;
-    uint4 u[U];
+    uint32_t u[U][N / 4];
     float s[U];
     bool ok[U];
 #pragma unroll
@@ -162,7 +230,8 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(KvView kv, DT* __r
       const int tok = tile * ROWS + vec / VPR;
       ok[v] = tok < T;
       s[v] = 0.f;
-      u[v] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int j = 0; j < N / 4; ++j) u[v][j] = 0u;
       if (!ok[v]) continue;
       size_t row, sidx;
       if (kv.page_size == 0) {
@@ -179,7 +248,14 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(KvView kv, DT* __r
         row = ((size_t)page * kv.n_kv + h) * kv.page_size + r;
         sidx = ((size_t)page * kv.n_kv + h) * kv.blocks_per_row + (r >> kv.block_shift);
       }
-      u[v] = *reinterpret_cast<const uint4*>(code + row * D + (vec % VPR) * 16);
+      const uint8_t* const from = code + row * D + (vec % VPR) * N;
+      if constexpr (N == 8) {
+        const uint2 w = *reinterpret_cast<const uint2*>(from);
+        u[v][0] = w.x;
+        u[v][N / 4 - 1] = w.y;
+      } else {
+        u[v][0] = *reinterpret_cast<const uint32_t*>(from);
+      }
       s[v] = scale[sidx];
     }
 #pragma unroll
@@ -187,31 +263,25 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(KvView kv, DT* __r
       if (!ok[v]) continue;
       const int vec = v * kThreads + threadIdx.x;
       const int tok = tile * ROWS + vec / VPR;
-      DT* const o = dst + (size_t)b * st.batch + (size_t)h * st.head + (size_t)tok * st.token + (vec % VPR) * 16;
-      const uint32_t w[4] = {u[v].x, u[v].y, u[v].z, u[v].w};
-      float x[16];
+      DT* const o = dst + (size_t)b * st.batch + (size_t)h * st.head + (size_t)tok * st.token + (vec % VPR) * N;
+      float x[N];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < N / 4; ++j) {
         float y[4];
-        decode4<CT>(w[j], y);
+        decode4<CT>(u[v][j], y);
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[4 * j + e] = y[e] * s[v];
       }
-      if constexpr (sizeof(DT) == 4) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          reinterpret_cast<float4*>(o)[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+      if constexpr (N == 4) {
+        *reinterpret_cast<float4*>(o) = make_float4(x[0], x[1], x[2], x[3]);
       } else {
+        uint32_t p[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint32_t p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 y = __floats2bfloat162_rn(x[8 * j + 2 * e], x[8 * j + 2 * e + 1]);
-            p[e] = *reinterpret_cast<const uint32_t*>(&y);
-          }
-          reinterpret_cast<uint4*>(o)[j] = make_uint4(p[0], p[1], p[2], p[3]);
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+          p[e] = *reinterpret_cast<const uint32_t*>(&y);
         }
+        *reinterpret_cast<uint4*>(o) = make_uint4(p[0], p[1], p[2], p[3]);
       }
     }
   }
@@ -298,15 +368,16 @@ __global__ void __launch_bounds__(kAppendThreads) append8_kernel(KvView kv, cons
 
 template <typename ST, typename CT, int D, int BL>
 cudaError_t quantize_t(const KvView& kv, const void* k, const void* v, Strides3 st, cudaStream_t s) {
-  constexpr int VB = BL * D / Vec<ST>::N;
-  constexpr int NV = VB <= 4 * kThreads ? 4 : VB / kThreads;
-  constexpr int BPC = kThreads / (VB / NV);
+  constexpr int BPC = QuantLayout<ST, CT, D, BL>::BPC;
   const int nb = (kv.t_max + BL - 1) / BL;
   const long long items = (long long)kv.batch * nb * kv.n_kv;
   const long long ctas = (items + BPC - 1) / BPC;
-  const int grid = (int)(ctas < (1 << 22) ? ctas : (1 << 22));
-  quantize_kernel<ST, CT, D, BL><<<dim3(grid, 2), kThreads, 0, s>>>(kv, static_cast<const ST*>(k),
-                                                                    static_cast<const ST*>(v), st, nb, items);
+  auto kern = quantize_kernel<ST, CT, D, BL>;
+  const int per_sm = prepare_kernel((const void*)kern, 0, kThreads);
+  if (per_sm < 1) return cudaErrorInvalidConfiguration;
+  const long long most = ((long long)sm_count() * per_sm + 1) / 2;   // of each side
+  kern<<<dim3((unsigned)(ctas < most ? ctas : most), 2), kThreads, 0, s>>>(kv, static_cast<const ST*>(k),
+                                                                           static_cast<const ST*>(v), st, nb, items);
   return cudaGetLastError();
 }
 
@@ -326,14 +397,22 @@ cudaError_t quantize_d(const KvView& kv, const void* k, const void* v, Strides3 
   return kv.head_dim == 64 ? quantize_b<ST, CT, 64>(kv, k, v, st, s) : quantize_b<ST, CT, 128>(kv, k, v, st, s);
 }
 
+template <typename DT, typename CT, int D, int UV>
+cudaError_t dequantize_u(const KvView& kv, void* k, void* v, Strides3 st, cudaStream_t s) {
+  constexpr int ROWS = DeqLayout<DT, D, UV>::ROWS;
+  const int tiles = (kv.t_max + ROWS - 1) / ROWS;
+  dequantize_kernel<DT, CT, D, UV><<<dim3(kv.batch * kv.n_kv, tiles < 65535 ? tiles : 65535, 2), kThreads, 0, s>>>(
+      kv, static_cast<DT*>(k), static_cast<DT*>(v), st, tiles);
+  return cudaGetLastError();
+}
+
+// Caches that would not fill the SMs with 8 vectors per thread take 2 (2 x 512 tokens, d = 64:
+// 2.9 against 4.4 us).
 template <typename DT, typename CT, int D>
 cudaError_t dequantize_t(const KvView& kv, void* k, void* v, Strides3 st, cudaStream_t s) {
-  constexpr int ROWS = 4 * kThreads / (D / 16);
-  const int tiles = (kv.t_max + ROWS - 1) / ROWS;
-  const long long items = (long long)kv.batch * kv.n_kv * tiles;
-  const int grid = (int)(items < (1 << 22) ? items : (1 << 22));
-  dequantize_kernel<DT, CT, D><<<dim3(grid, 2), kThreads, 0, s>>>(kv, static_cast<DT*>(k), static_cast<DT*>(v), st, tiles);
-  return cudaGetLastError();
+  constexpr int ROWS = DeqLayout<DT, D, 8>::ROWS;
+  const long long ctas = 2LL * kv.batch * kv.n_kv * ((kv.t_max + ROWS - 1) / ROWS);
+  return ctas < sm_count() ? dequantize_u<DT, CT, D, 2>(kv, k, v, st, s) : dequantize_u<DT, CT, D, 8>(kv, k, v, st, s);
 }
 
 template <typename DT, typename CT>

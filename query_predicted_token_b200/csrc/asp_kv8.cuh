@@ -15,6 +15,24 @@ namespace asp {
 struct CodeE4M3 {
   // frexp mantissa of the largest code, 448 = 0.875 * 2^9: the fraction bits above
   // which a value needs the next power of two, and the exponent it is taken off
+  // packed magnitudes of four codes, and whether one of them is NaN
+  __device__ __forceinline__ static uint32_t mag4(uint32_t w) { return w & 0x7f7f7f7fu; }
+  static constexpr uint32_t kNanMag = 0x7fu;
+  __device__ __forceinline__ static float mag_value(uint32_t m) {   // of one magnitude
+    const uint32_t h = pair(m, 0);
+    return __half2float(__ushort_as_half((unsigned short)h));
+  }
+  // four codes times a power of two f in [2^-24, 2^15], encoded again: every product that is
+  // not exact in fp16 rounds to the code 0 either way
+  __device__ __forceinline__ static uint32_t rescale4(uint32_t w, __half2 f) {
+    const uint32_t a = pair(w, 0), b = pair(w, 1);
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&a), f);
+    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&b), f);
+    unsigned short lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(*reinterpret_cast<const uint32_t*>(&y)));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+  }
   static constexpr uint32_t kTopFrac = 0x600000u;
   static constexpr int kShift = 9;
   // two codes (low, high byte) -> fp16x2 (low, high half), exact
@@ -35,6 +53,16 @@ struct CodeE4M3 {
 };
 
 struct CodeI8 {
+  __device__ __forceinline__ static uint32_t mag4(uint32_t w) { return __vabs4(w); }
+  static constexpr uint32_t kNanMag = 0x1ffu;   // none
+  __device__ __forceinline__ static float mag_value(uint32_t m) { return (float)m; }
+  // as above; 1536 + x rounds x to an integer, whose low byte is then the code's
+  __device__ __forceinline__ static uint32_t rescale4(uint32_t w, __half2 f) {
+    const uint32_t p = prep(w), a = pair(p, 0), b = pair(p, 1), m = 0x66006600u;
+    const __half2 x = __hfma2(*reinterpret_cast<const __half2*>(&a), f, *reinterpret_cast<const __half2*>(&m));
+    const __half2 y = __hfma2(*reinterpret_cast<const __half2*>(&b), f, *reinterpret_cast<const __half2*>(&m));
+    return __byte_perm(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y), 0x6420);
+  }
   static constexpr uint32_t kTopFrac = 0x7e0000u;   // 127 = 0.9921875 * 2^7
   static constexpr int kShift = 7;
   // The biased byte u = code + 128 below the fp16 pattern 0x6400 is 1024 + u; less 1152
