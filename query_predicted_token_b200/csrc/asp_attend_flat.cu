@@ -32,6 +32,8 @@ namespace asp {
 namespace {
 
 constexpr int kTile = 16;
+constexpr int kWarps = 8;                  // of a CTA
+constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 2;
 constexpr int kMinTiles = 8;               // of a CTA's range
 constexpr int kFlatSms = 148;
@@ -117,8 +119,7 @@ template <typename CT>
 struct Fmt {   // 8-bit codes, fp16 products
   static constexpr int kEB = 1;
   static constexpr bool kScaled = true;
-  static constexpr int kWarps = 8, kCtas = 2;    // of a CTA; CTAs per SM
-  static constexpr int kMergeHeads = 8;          // heads joined together at a unit's end
+  static constexpr int kCtas = 2;                // per SM
   __device__ __forceinline__ static void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -139,8 +140,7 @@ template <>
 struct Fmt<__nv_bfloat16> {
   static constexpr int kEB = 2;
   static constexpr bool kScaled = false;
-  static constexpr int kWarps = 12, kCtas = 1;
-  static constexpr int kMergeHeads = 4;          // shared memory holds the stages and no more
+  static constexpr int kCtas = 1;
   __device__ __forceinline__ static void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -186,42 +186,69 @@ struct Stage {
 };
 
 __host__ __device__ constexpr int mo_stride(int D) { return D + 4; }
-template <typename CT>
-__host__ __device__ constexpr int merge_heads(int G) { return G < Fmt<CT>::kMergeHeads ? G : Fmt<CT>::kMergeHeads; }
 template <typename CT, int D>
 constexpr size_t flat_smem(int G) {
-  return (size_t)Fmt<CT>::kWarps * (kStages * Stage<CT, D>::BYTES + (merge_heads<CT>(G) * mo_stride(D) + 4 * G) * 4);
+  return (size_t)kWarps * (kStages * Stage<CT, D>::BYTES + G * (mo_stride(D) + 4) * 4);
 }
 
-// acc of the rows r, r + kFinThreads, ... (VECS of them, below r1): the weights of the group's
-// heads, each from its logit by `weight`.  Rows that were not attended hold -inf.
-constexpr int kAccVecs = 4;
-constexpr int kAccRows = kAccVecs * kFinThreads;
+// The logits of rows r .. r + 3 (r a multiple of 4), one vector per head; rows past the unit's
+// and rows that were not attended hold -inf.
+constexpr int kAccRows = 4 * kFinThreads;   // of a CTA of finish_kernel
 
-template <int VECS, typename W>
-__device__ __forceinline__ void add_weights(const FlatParams& p, int u, const UnitRows& ur, int r, int r1, W weight) {
-  float x[VECS][8];
-  int tok[VECS];
+struct RowLogits {
+  float4 x[8];
+  int tok[4];          // -1: not a row
+  bool run;            // four tokens that follow one another, on a 16-byte boundary of acc
+};
+
+__device__ __forceinline__ void load_logits(const FlatParams& p, int u, const UnitRows& ur, int r, RowLogits& q) {
+  q.run = false;
 #pragma unroll
-  for (int k = 0; k < VECS; ++k) {
-    const int rk = r + k * kFinThreads;
-    tok[k] = -1;
-    if (rk >= r1) continue;
-    tok[k] = rk < ur.n_sel ? p.idx[(size_t)u * p.C + rk] : ur.tb + (rk - ur.n_sel);
+  for (int k = 0; k < 4; ++k) q.tok[k] = -1;
+  if (r >= ur.n_rows) return;
 #pragma unroll
-    for (int gg = 0; gg < 8; ++gg)
-      if (gg < p.G) x[k][gg] = p.logits[((size_t)u * p.G + gg) * p.row_stride + rk];
-  }
+  for (int gg = 0; gg < 8; ++gg)
+    if (gg < p.G) q.x[gg] = *reinterpret_cast<const float4*>(p.logits + ((size_t)u * p.G + gg) * p.row_stride + r);
 #pragma unroll
-  for (int k = 0; k < VECS; ++k) {
-    if (tok[k] < 0 || x[k][0] == -INFINITY) continue;
-    float w = 0.f;
-#pragma unroll
-    for (int gg = 0; gg < 8; ++gg)
-      if (gg < p.G) w += weight(gg, x[k][gg]);
-    atomicAdd(p.acc + (size_t)u * p.t_max + tok[k], w);
-  }
+  for (int k = 0; k < 4; ++k)
+    if (r + k < ur.n_rows)
+      q.tok[k] = r + k < ur.n_sel ? p.idx[(size_t)u * p.C + r + k] : ur.tb + (r + k - ur.n_sel);
+  q.run = r >= ur.n_sel && r + 3 < ur.n_rows &&
+          (reinterpret_cast<uintptr_t>(p.acc + (size_t)u * p.t_max + q.tok[0]) & 15) == 0;
 }
+
+// acc of those rows: the weights of the group's heads, each from its logit by `weight`.
+template <typename W>
+__device__ __forceinline__ void add_weights(const FlatParams& p, int u, const RowLogits& q, W weight) {
+  float w[4] = {0.f, 0.f, 0.f, 0.f};
+  bool has[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    has[k] = q.tok[k] >= 0 && (k == 0 ? q.x[0].x : k == 1 ? q.x[0].y : k == 2 ? q.x[0].z : q.x[0].w) != -INFINITY;
+  if (!(has[0] || has[1] || has[2] || has[3])) return;
+#pragma unroll
+  for (int gg = 0; gg < 8; ++gg)
+    if (gg < p.G) {
+      w[0] += weight(gg, q.x[gg].x);
+      w[1] += weight(gg, q.x[gg].y);
+      w[2] += weight(gg, q.x[gg].z);
+      w[3] += weight(gg, q.x[gg].w);
+    }
+  float* const acc = p.acc + (size_t)u * p.t_max;
+  if (q.run && has[0] && has[1] && has[2] && has[3]) {
+    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(acc + q.tok[0]), "f"(w[0]), "f"(w[1]), "f"(w[2]),
+                 "f"(w[3])
+                 : "memory");
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (has[k]) atomicAdd(acc + q.tok[k], w[k]);
+}
+
+// Barrier 1 of the CTA: the joiner of a unit waits, the other warps only arrive.
+__device__ __forceinline__ void joiner_wait() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+__device__ __forceinline__ void joiner_arrive() { asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory"); }
 
 // Transposes an 8x8 matrix of 16-bit values held two per lane.
 __device__ __forceinline__ uint32_t movm(uint32_t a) {
@@ -232,10 +259,10 @@ __device__ __forceinline__ uint32_t movm(uint32_t a) {
 
 // QP: parts of the query (8-bit caches: 1 for bf16, 2 for fp32; bf16 caches: 1 or 3).
 template <typename CT, int D, int QP, bool ACC>
-__global__ void __launch_bounds__(Fmt<CT>::kWarps * 32, Fmt<CT>::kCtas) attend_flat_kernel(FlatParams p) {
+__global__ void __launch_bounds__(kThreads, Fmt<CT>::kCtas) attend_flat_kernel(FlatParams p) {
   using F = Fmt<CT>;
   using S = Stage<CT, D>;
-  constexpr int W = F::kWarps, THREADS = W * 32;
+  constexpr int W = kWarps, THREADS = kThreads;
   constexpr int KS = D / 16;                 // k-steps of the logits
   constexpr int MT = D / 16;                 // m-tiles of the output
   constexpr bool WSPLIT = !F::kScaled || QP > 1;   // weights in two parts
@@ -244,13 +271,12 @@ __global__ void __launch_bounds__(Fmt<CT>::kWarps * 32, Fmt<CT>::kCtas) attend_f
   __shared__ int run_pre[THREADS + 1];
   __shared__ int scan[33];
   __shared__ int s_first[2];
-  __shared__ float4 s_unit[8];               // of the unit's heads: m, l, M, 1 / (l 2^..)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int G = p.G, GM = merge_heads<CT>(G);
+  const int G = p.G;
   uint8_t* const ring = smem + (size_t)warp * kStages * S::BYTES;
-  float* const mo = reinterpret_cast<float*>(smem + (size_t)W * kStages * S::BYTES);   // [warp][GM][D + 4]
-  float* const mml = mo + (size_t)W * GM * mo_stride(D);                               // [warp][G][4]
+  float* const mo = reinterpret_cast<float*>(smem + (size_t)W * kStages * S::BYTES);   // [warp][G][D + 4]
+  float* const mml = mo + (size_t)W * G * mo_stride(D);                                // [warp][G][4]
 
   pdl_wait();
 
@@ -500,6 +526,7 @@ __global__ void __launch_bounds__(Fmt<CT>::kWarps * 32, Fmt<CT>::kCtas) attend_f
 
   // ---- the tiles of each unit in turn
   int j = 0;                 // this warp's next tile
+  int seg = 0;               // units so far
   int seg_t0 = t0 - tl0;     // where the current unit's tiles begin in the flattened order
   for (int u = u0;; ++u) {
     const UnitRows ur = unit_rows(p, u, false);
@@ -507,6 +534,12 @@ __global__ void __launch_bounds__(Fmt<CT>::kWarps * 32, Fmt<CT>::kCtas) attend_f
     const int seg_end = min(t1, seg_t0 + un);
     const int kend = seg_end - t0 - warp;
     const int jend = kend > 0 ? (kend + W - 1) / W : 0;
+    if (seg_end < t1) {      // the next unit's query towards L1
+      const int nb = (u + 1) / p.n_kv, nh = u + 1 - nb * p.n_kv;
+      const int es = p.q_f32 ? 4 : 2;
+      const uint8_t* const next = static_cast<const uint8_t*>(p.q) + ((size_t)nb * p.n_q_heads + nh * G) * D * es;
+      if (lane * 128 < G * D * es) asm volatile("prefetch.global.L1 [%0];" ::"l"(next + lane * 128));
+    }
     float o[MT][4];
 #pragma unroll
     for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -703,88 +736,97 @@ __global__ void __launch_bounds__(Fmt<CT>::kWarps * 32, Fmt<CT>::kCtas) attend_f
       if constexpr (!F::kScaled) M[e] = m[e];
     }
 
-    // ---- the warps' results of this unit meet in shared memory: the statistics first, then
-    // the outputs at a common scale, up to GM heads at a time; position 16 i + 2 g + e of a
-    // head's row is channel v_chan(i, g, e)
+    // ---- the warps' results of this unit meet in shared memory (position 16 i + 2 g + e of a
+    // head's row is channel v_chan(i, g, e)), and one warp, another for each unit, joins them
+    // while the others go on with the next unit.  Barrier 1: the results are there.  Every warp,
+    // the last joiner too, meets the others before the buffer is written again: a warp that
+    // did not could arrive at a barrier's phase before the one meant for it.
+    const int joiner = seg % W;
+    if (seg > 0) __syncthreads();
     if (g == 0) {
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         if (2 * t + e < G)
           *reinterpret_cast<float4*>(mml + (warp * G + 2 * t + e) * 4) = make_float4(m[e], l[e], M[e], 0.f);
     }
-    __syncthreads();
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      if (2 * t + e >= G) continue;
-      float MM = kLowest;
+      if (2 * t + e < G) {
+        float* const row = mo + ((size_t)warp * G + 2 * t + e) * mo_stride(D) + 2 * g;
 #pragma unroll
-      for (int w = 0; w < W; ++w) MM = fmaxf(MM, mml[(w * G + 2 * t + e) * 4 + 2]);
-      const float f = ex2(M[e] - MM);   // a warp without rows: o = 0
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        o[i][e] *= f;
-        o[i][2 + e] *= f;
+        for (int i = 0; i < MT; ++i) *reinterpret_cast<float2*>(row + 16 * i) = make_float2(o[i][e], o[i][2 + e]);
       }
     }
-    auto put = [&](int h0) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int hm = 2 * t + e - h0;
-        if (hm >= 0 && hm < GM) {
-          float* const row = mo + ((size_t)warp * GM + hm) * mo_stride(D) + 2 * g;
-#pragma unroll
-          for (int i = 0; i < MT; ++i) *reinterpret_cast<float2*>(row + 16 * i) = make_float2(o[i][e], o[i][2 + e]);
-        }
-      }
-    };
-    put(0);
-    if (threadIdx.x < G) {
-      float mm = kLowest, MM = kLowest, L = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        mm = fmaxf(mm, mml[(w * G + threadIdx.x) * 4]);
-        MM = fmaxf(MM, mml[(w * G + threadIdx.x) * 4 + 2]);
-      }
-#pragma unroll
-      for (int w = 0; w < W; ++w) L += mml[(w * G + threadIdx.x) * 4 + 1] * ex2(mml[(w * G + threadIdx.x) * 4] - mm);
-      s_unit[threadIdx.x] = make_float4(mm, L, MM, L == 0.f ? 0.f : ex2(MM - mm - (F::kScaled ? (float)kWBias : 0.f)) / L);
-    }
-    __syncthreads();
     const bool last = seg_end >= t1;
-    const bool starts = seg_t0 >= t0, ends = seg_t0 + un <= t1;
-    const bool alone = starts && ends;
-    const int slot = 2 * cta + (u == u0 ? 0 : 1);
-    if (!p.whole && starts && threadIdx.x == 0)
-      p.info[u] = make_int4(cta, ends ? cta : range_owner(seg_t0 + un - 1, total, N), slot, 0);
-    const int b = u / p.n_kv, h = u - b * p.n_kv;
-    for (int h0 = 0; h0 < G; h0 += GM) {
-      if (h0) {
-        __syncthreads();
-        put(h0);
-        __syncthreads();
-      }
-      for (int e = threadIdx.x; e < GM * D; e += THREADS) {
-        const int hm = e / D, pos = e - hm * D, gg = h0 + hm;
-        const int c = S::v_chan(pos >> 4, (pos & 15) >> 1, pos & 1);
-        float O = 0.f;
+    __syncwarp();
+    if (warp != joiner) {
+      joiner_arrive();
+    } else {
+      joiner_wait();
+      const bool starts = seg_t0 >= t0, ends = seg_t0 + un <= t1;
+      const bool alone = starts && ends;
+      const int slot = 2 * cta + (u == u0 ? 0 : 1);
+      if (!p.whole && starts && lane == 0)
+        p.info[u] = make_int4(cta, ends ? cta : range_owner(seg_t0 + un - 1, total, N), slot, 0);
+      const int b = u / p.n_kv, h = u - b * p.n_kv;
+      for (int gg = 0; gg < G; ++gg) {
+        // lane w: warp w's statistics of the head and the factor of its output (l = 0, o = 0
+        // for a warp without rows)
+        float4 ml = make_float4(kLowest, 0.f, kLowest, 0.f);
+        if (lane < W) ml = *reinterpret_cast<const float4*>(mml + (lane * G + gg) * 4);
+        float mm = ml.x, MM = ml.z;
 #pragma unroll
-        for (int w = 0; w < W; ++w) O += mo[((size_t)w * GM + hm) * mo_stride(D) + pos];
-        const float4 un4 = s_unit[gg];
+        for (int sh = W / 2; sh; sh >>= 1) {
+          mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, sh));
+          MM = fmaxf(MM, __shfl_xor_sync(0xffffffffu, MM, sh));
+        }
+        mm = __shfl_sync(0xffffffffu, mm, 0);
+        MM = __shfl_sync(0xffffffffu, MM, 0);
+        const float fw = ex2(ml.z - MM);
+        float L = ml.y * ex2(ml.x - mm);
+#pragma unroll
+        for (int sh = W / 2; sh; sh >>= 1) L += __shfl_xor_sync(0xffffffffu, L, sh);
+        L = __shfl_sync(0xffffffffu, L, 0);
+        float f[W];
+#pragma unroll
+        for (int w = 0; w < W; ++w) f[w] = __shfl_sync(0xffffffffu, fw, w);
+        const float scale = L == 0.f ? 0.f : ex2(MM - mm - (F::kScaled ? (float)kWBias : 0.f)) / L;
         const size_t bh = (size_t)b * p.n_q_heads + h * G + gg;
-        if (alone) {
-          const float y = un4.y == 0.f ? 0.f : O * un4.w;
-          if (p.out_f32) static_cast<float*>(p.out)[bh * D + c] = y;
-          else static_cast<__nv_bfloat16*>(p.out)[bh * D + c] = __float2bfloat16_rn(y);
-          if (pos == 0) {
-            if (p.lse) p.lse[bh] = un4.y == 0.f ? -INFINITY : un4.x * kLn2 + logf(un4.y);
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) {   // two channels per lane
+          const int pos = 64 * k + 2 * lane;
+          const int c = S::v_chan(pos >> 4, (pos & 15) >> 1, 0);
+          float2 O = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            const float2 x = *reinterpret_cast<const float2*>(mo + ((size_t)w * G + gg) * mo_stride(D) + pos);
+            O.x += x.x * f[w];
+            O.y += x.y * f[w];
+          }
+          if (alone) {
+            if (L == 0.f) O = make_float2(0.f, 0.f);
+            else O = make_float2(O.x * scale, O.y * scale);
+            if (p.out_f32) {
+              static_cast<float*>(p.out)[bh * D + c] = O.x;
+              static_cast<float*>(p.out)[bh * D + c + 1] = O.y;
+            } else {
+              static_cast<__nv_bfloat16*>(p.out)[bh * D + c] = __float2bfloat16_rn(O.x);
+              static_cast<__nv_bfloat16*>(p.out)[bh * D + c + 1] = __float2bfloat16_rn(O.y);
+            }
+          } else {
+            *reinterpret_cast<float2*>(p.part_o + ((size_t)slot * G + gg) * D + c) = O;
+          }
+        }
+        if (lane == 0) {
+          if (!alone) {
+            *reinterpret_cast<float4*>(p.part_ml + ((size_t)slot * G + gg) * 4) = make_float4(mm, L, MM, 0.f);
+          } else {
+            if (p.lse) p.lse[bh] = L == 0.f ? -INFINITY : mm * kLn2 + logf(L);
             if constexpr (ACC) {
-              p.stat[((size_t)u * G + gg) * 2] = un4.x;
-              p.stat[((size_t)u * G + gg) * 2 + 1] = un4.y == 0.f ? 0.f : 1.f / un4.y;
+              p.stat[((size_t)u * G + gg) * 2] = mm;
+              p.stat[((size_t)u * G + gg) * 2 + 1] = L == 0.f ? 0.f : 1.f / L;
             }
           }
-        } else {
-          p.part_o[((size_t)slot * G + gg) * D + c] = O;
-          if (pos == 0) *reinterpret_cast<float4*>(p.part_ml + ((size_t)slot * G + gg) * 4) = un4;
         }
       }
     }
@@ -792,15 +834,21 @@ __global__ void __launch_bounds__(Fmt<CT>::kWarps * 32, Fmt<CT>::kCtas) attend_f
       if (p.whole) {   // this CTA holds every logit of the unit: the weights right away
         __syncthreads();
         const float* const stat = p.stat + (size_t)u * G * 2;
-        for (int r = threadIdx.x; r < ur.n_rows; r += THREADS)
-          add_weights<1>(p, u, ur, r, ur.n_rows, [&](int gg, float xv) { return ex2(xv - stat[2 * gg]) * stat[2 * gg + 1]; });
+        for (int r = threadIdx.x; r < ur.n_rows; r += THREADS) {   // few rows: one at a time, in few registers
+          const float* const x = p.logits + (size_t)u * G * p.row_stride + r;
+          if (x[0] == -INFINITY) continue;
+          float w = 0.f;
+#pragma unroll 1
+          for (int gg = 0; gg < G; ++gg) w += ex2(x[(size_t)gg * p.row_stride] - stat[2 * gg]) * stat[2 * gg + 1];
+          const int tok = r < ur.n_sel ? p.idx[(size_t)u * p.C + r] : ur.tb + (r - ur.n_sel);
+          atomicAdd(p.acc + (size_t)u * p.t_max + tok, w);
+        }
       }
     }
     if (last) break;
     load_q(u + 1);
-    // no barrier here: mml was read before the last one, and mo and s_unit are written again
-    // after the next unit's first
     seg_t0 += un;
+    ++seg;
   }
 }
 
@@ -822,6 +870,8 @@ __global__ void __launch_bounds__(kFinThreads) finish_kernel(FlatParams p, float
     ur = unit_rows(p, u, false);
     if (!join && (int)blockIdx.y * kAccRows >= ur.n_rows) return;
   }
+  RowLogits rows;   // requested ahead of the statistics
+  if constexpr (ACC) load_logits(p, u, ur, blockIdx.y * kAccRows + 4 * threadIdx.x, rows);
   auto slot_of = [&](int i) -> int { return i == 0 ? in.z : 2 * (in.x + i); };
   if (warp < G) {   // warp gg: statistics of head gg
     if (n > 1) {
@@ -896,9 +946,7 @@ __global__ void __launch_bounds__(kFinThreads) finish_kernel(FlatParams p, float
     __syncthreads();
     if (n > 1 && threadIdx.x < G) s_l[threadIdx.x] = s_l[threadIdx.x] == 0.f ? 0.f : 1.f / s_l[threadIdx.x];
     __syncthreads();
-    const int r1 = min(ur.n_rows, ((int)blockIdx.y + 1) * kAccRows);
-    add_weights<kAccVecs>(p, u, ur, blockIdx.y * kAccRows + threadIdx.x, r1,
-                [&](int gg, float xv) { return ex2(xv - s_m[gg]) * s_l[gg]; });
+    add_weights(p, u, rows, [&](int gg, float xv) { return ex2(xv - s_m[gg]) * s_l[gg]; });
   }
 }
 
@@ -910,19 +958,19 @@ __global__ void __launch_bounds__(kFinThreads) accumulate_kernel(FlatParams p) {
   pdl_wait();
   const UnitRows ur = unit_rows(p, u, false);
   if ((int)blockIdx.y * kAccRows >= ur.n_rows) return;
+  RowLogits rows;
+  load_logits(p, u, ur, blockIdx.y * kAccRows + 4 * threadIdx.x, rows);
   if (threadIdx.x < G) s_l[threadIdx.x] = p.lse[(size_t)b * p.n_q_heads + h * G + threadIdx.x];
   __syncthreads();
-  const int r1 = min(ur.n_rows, ((int)blockIdx.y + 1) * kAccRows);
-  add_weights<kAccVecs>(p, u, ur, blockIdx.y * kAccRows + threadIdx.x, r1,
-              [&](int gg, float xv) { return expf(xv * kLn2 - s_l[gg]); });
+  add_weights(p, u, rows, [&](int gg, float xv) { return expf(xv * kLn2 - s_l[gg]); });
 }
 
 template <typename CT, int D, int QP, bool ACC>
 cudaError_t launch_flat_t(const FlatParams& p, int ctas, int chunks, cudaStream_t s) {
   auto kern = attend_flat_kernel<CT, D, QP, ACC>;
   const size_t smem = flat_smem<CT, D>(p.G);
-  if (prepare_kernel((const void*)kern, smem, Fmt<CT>::kWarps * 32) < 1) return cudaErrorInvalidConfiguration;
-  cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(Fmt<CT>::kWarps * 32), smem, s, p);
+  if (prepare_kernel((const void*)kern, smem, kThreads) < 1) return cudaErrorInvalidConfiguration;
+  cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, s, p);
   if (e != cudaSuccess || p.whole) return e;
   return launch_pdl(finish_kernel<D, ACC>, dim3(p.units, ACC ? chunks : 1), dim3(kFinThreads), 0, s, p,
                     Fmt<CT>::kScaled ? (float)kWBias : 0.f);
