@@ -100,9 +100,9 @@ typedef enum { ASP_POOL_PREDICTIONS = 0, ASP_POOL_FEATURES = 1 } asp_pool_mode;
 #define ASP_DEV_TAIL_LIMIT 0x8   /* a tail longer than max_tail was truncated */
 #define ASP_DEV_SELECT     0x10  /* a selection output position past C was skipped (a first-digit
                                     histogram that does not match the scores) */
-#define ASP_DEV_NONFINITE  0x40  /* an infinity or NaN was written to an 8-bit cache (see asp_quantize_kv) */
 #define ASP_DEV_NAN_SCORE  0x20  /* the selection read a NaN score: invalid input, the chosen set
                                     is then unspecified (it never holds more than C tokens) */
+#define ASP_DEV_NONFINITE  0x40  /* an infinity or NaN was written to an 8-bit cache (see asp_quantize_kv) */
 
 /* The KV cache of one layer.
  *   page_size == 0: k, v are [batch, n_kv_heads, t_max, head_dim] (contiguous).
@@ -186,8 +186,9 @@ ASP_API asp_status asp_predict_query(float* qhist, int ring_start, const void* q
  * scores[b, h, j] = max over the G query heads g of KV head h of
  *                   (qpred[b, h*G + g, :] . k[b, h, j, :]) / sqrt(head_dim),  j < T_b.
  * Entries j >= T_b of a row are not written.  fp32 arithmetic.  8-bit caches: k is
- * code * scale; every product of a code with the query (two fp16 parts: 22 bits of each
- * head's largest channel) is exact in the fp32 sum, which the scale then multiplies.
+ * code * scale; the query enters as 22 bits of each head's largest channel (two fp16 parts,
+ * or three 8-bit digits for ASP_I8), its products with the codes are exact, and the scale
+ * multiplies their sum.
  * qpred  : device fp32 [batch, n_q_heads, head_dim].
  * scores : device fp32 [batch, n_kv_heads, t_max], written.
  * Errors: ASP_ERR_INVALID_ARG; ASP_ERR_UNSUPPORTED (G not in {1,2,4,8}, head_dim
@@ -197,9 +198,9 @@ ASP_API asp_status asp_score_keys(const float* qpred, int n_q_heads, const asp_k
 
 /* Step 2 on the CUDA cores whatever the key type: the scan asp_score_keys runs for
  * fp32 keys and page sizes other than 16, and for bf16 keys the comparison of its
- * tensor-core scan; not for 8-bit caches (same arguments, errors and results within the score tolerance;
- * the tensor-core path replaced it for bf16 keys because it reaches the copy
- * bandwidth where this one is bound by instruction issue). */
+ * tensor-core scan; not for 8-bit caches (same arguments, errors and results within the
+ * score tolerance; the tensor-core path replaced it for bf16 keys because it reaches the
+ * copy bandwidth where this one is bound by instruction issue). */
 ASP_API asp_status asp_score_keys_cuda_cores(const float* qpred, int n_q_heads, const asp_kv* kv, float* scores,
                                              asp_stream_t stream);
 
@@ -365,7 +366,8 @@ ASP_API asp_status asp_dequantize_kv(const asp_kv* kv, void* k_dst, void* v_dst,
  * workspace  : asp_accumulate_workspace_bytes(...) bytes, 256-byte aligned, no
  *              initialisation needed; it holds the logits between the passes.  Two calls
  *              that may overlap (streams, captured graphs) need workspaces of their own.
- * Other arguments and errors as asp_sparse_attend. */
+ * Other arguments and errors as asp_sparse_attend; for an fp32 cache q must be 16-byte
+ * aligned (ASP_ERR_INVALID_ARG). */
 ASP_API asp_status asp_attend_accumulate(const void* q, asp_dtype q_dtype, int n_q_heads, const asp_kv* kv,
                                          const int32_t* idx, const int32_t* count, int C, const int32_t* tail_begin,
                                          int max_tail, void* out, float* lse, float* acc, void* workspace,

@@ -441,6 +441,7 @@ asp_status asp_attend_accumulate(const void* q, asp_dtype q_dtype, int n_q_heads
                                ~static_cast<size_t>(0), &plan, 0, &flat);
   if (st != ASP_OK) return st;
   if (!acc) return ASP_ERR_INVALID_ARG;
+  if (kv->kv_dtype == ASP_F32 && !aligned16(q)) return ASP_ERR_INVALID_ARG;   // read by whole vectors
   const int mt = tail_begin ? max_tail : 0;
   const size_t need = asp_accumulate_workspace_bytes(kv, n_q_heads, C, mt);
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)) return ASP_ERR_WORKSPACE;

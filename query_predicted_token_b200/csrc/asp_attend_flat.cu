@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, Fmt<CT>::kCtas) attend_flat_kernel(F
             }
           }
         }
-        float ve[2], vmant[2];   // V's scale of rows g and g + 8: 2^23 + its biased exponent, and its fraction
+        float ve[2], vmant[2];   // V's scale of rows g and g + 8: exponent and fraction
         if constexpr (F::kScaled) {
           const float* const ksc = reinterpret_cast<const float*>(st + S::SCALES);
 #pragma unroll
@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, Fmt<CT>::kCtas) attend_flat_kernel(F
             x[2 * r] *= k * qfac[0];
             x[2 * r + 1] *= k * qfac[1];
             const uint32_t bits = __float_as_uint(ksc[16 + 8 * r + g]);
-            ve[r] = __uint_as_float((bits >> 23) | 0x4b000000u);
+            ve[r] = __uint_as_float((bits >> 23) | 0x4b000000u) - 8388735.f;   // 2^23 + 127
             vmant[r] = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
           }
         } else {
@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, Fmt<CT>::kCtas) attend_flat_kernel(F
         auto exponents = [&]() {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float off = (float)kWBias - 8388735.f - M[e];   // integers below 2^24: exact
+            const float off = (float)kWBias - M[e];   // integers: exact
             a[e] = x[e] + (ve[0] + off);
             a[2 + e] = x[2 + e] + (ve[1] + off);
           }
@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, Fmt<CT>::kCtas) attend_flat_kernel(F
             l[e] *= corr[e];
             m[e] = mn;
             if constexpr (F::kScaled) {
-              float Mr = fmaxf(x[e] + (ve[0] - 8388735.f), x[2 + e] + (ve[1] - 8388735.f));
+              float Mr = fmaxf(x[e] + ve[0], x[2 + e] + ve[1]);
               Mr = fmaxf(Mr, __shfl_xor_sync(0xffffffffu, Mr, 4));
               Mr = fmaxf(Mr, __shfl_xor_sync(0xffffffffu, Mr, 8));
               Mr = fmaxf(Mr, __shfl_xor_sync(0xffffffffu, Mr, 16));

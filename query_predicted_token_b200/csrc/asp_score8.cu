@@ -45,6 +45,7 @@ struct Score8Params {
   float* scores;
   int32_t* hist;
   float scale;
+  int stages;          // of a warp's ring
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -264,7 +265,7 @@ struct Query<CodeI8, D, NT> {     // NT = 3: column g of n-tile n is digit n (hi
 
 template <int D>
 struct Ring {                          // of a warp
-  static constexpr int STAGES = 3;
+  static constexpr int STAGES = 3;                   // at most; two where a large batch's lengths need the room
   static constexpr int ROWS = kRows * D;             // bytes of a step's rows
   static constexpr int BYTES = ROWS + 16;            // and where its tiles' scales lie
 };
@@ -273,10 +274,10 @@ template <typename CT, int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, 1) score8_kernel(Score8Params p) {
   using R = Ring<D>;
   constexpr int LD = D / 64;           // 16-byte pieces of a row per lane
-  constexpr int S = R::STAGES;
+  const int S = p.stages;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int scratch[33];
-  __shared__ uint64_t bars_all[kWarps * S];
+  __shared__ uint64_t bars_all[kWarps * R::STAGES];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   uint8_t* const ring = smem + (size_t)warp * S * R::BYTES;
@@ -414,13 +415,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) score8_kernel(Score8Params p) 
   };
   float n_scale = scale_of(0);
 #pragma unroll 1
-  for (int i = 0, slot = 0; i < n; ++i, slot = slot + 1 == S ? 0 : slot + 1) {
+  for (int i = 0, slot = 0, phase = 0; i < n; ++i) {
     if (cc.b != qb || cc.h != qh) {
       qb = cc.b;
       qh = cc.h;
       q.load(p, qb, qh, g, t);
     }
-    ok = __all_sync(0xffffffffu, mbar_wait(&bars[slot], (uint32_t)(i / S) & 1u));
+    ok = __all_sync(0xffffffffu, mbar_wait(&bars[slot], (uint32_t)phase));
     if (!ok) break;
     const uint8_t* const st = ring + slot * R::BYTES;
     const float sc = n_scale;
@@ -465,6 +466,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) score8_kernel(Score8Params p) 
       }
     }
     advance(cc);
+    if (++slot == S) {
+      slot = 0;
+      phase ^= 1;
+    }
   }
   if (!ok) {   // a wait ran out: give the copies in flight a bounded chance to land
     for (int i = max(0, issued - S); i < issued; ++i) mbar_wait(&bars[i % S], (uint32_t)(i / S) & 1u);
@@ -472,11 +477,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) score8_kernel(Score8Params p) 
 }
 
 template <typename CT, int D, int NT>
-cudaError_t launch_t(const Score8Params& p, cudaStream_t s) {
+cudaError_t launch_t(Score8Params p, cudaStream_t s) {
   auto kern = score8_kernel<CT, D, NT>;
-  const size_t smem = (size_t)kWarps * Ring<D>::STAGES * Ring<D>::BYTES + (2 * (size_t)p.batch + 1) * 4;
-  const int per_sm = prepare_kernel((const void*)kern, smem, kWarps * 32);
-  if (per_sm < 1) return cudaErrorInvalidConfiguration;
+  const size_t stage = (size_t)kWarps * Ring<D>::BYTES, lens = (2 * (size_t)p.batch + 1) * 4;
+  constexpr size_t kRoom = 224 * 1024;   // of the 227 KB a CTA may have; the rest holds the barriers
+  p.stages = Ring<D>::STAGES * stage + lens <= kRoom ? Ring<D>::STAGES : 2;
+  const size_t smem = p.stages * stage + lens;
+  if (prepare_kernel((const void*)kern, smem, kWarps * 32) < 1) return cudaErrorInvalidConfiguration;
   return launch_pdl(kern, dim3(sm_count()), dim3(kWarps * 32), smem, s, p);
 }
 

@@ -101,6 +101,8 @@ def test_accumulate_arguments(lib, dtype):
     assert call(q=None) == INV
     assert call(out=None) == INV
     assert call(idx=None) == INV
+    if dtype == L.ASP_F32:
+        assert call(q=FAKE + 4) == INV         # an fp32 cache's kernel reads the query by whole vectors
     assert call(hq=7) == INV
     assert call(hq=6) == UNS
     assert call(C=0, tb=None) == INV           # nothing to attend

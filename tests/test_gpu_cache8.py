@@ -336,6 +336,39 @@ def test_score_keys_of_many_short_sequences():
             assert np.isnan(got[b, h, n:]).all()
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_score_keys_of_the_largest_batch(fmt):
+    """8192 sequences: the lengths in shared memory leave room for fewer stages."""
+    B, T, d = 8192, 40, 128
+    lens = [int(n) for n in np.random.default_rng(4).integers(0, T + 1, B)]
+    c = Cache(fmt, B, 1, d, T, lens, 0, 32, seed=2)
+    q = torch.randn(B, 2, d, generator=gen(5)).to(DEV)
+    scores = torch.full((B, 1, T), float("nan"), device=DEV)
+    asp.score_keys(q, c.kv, scores)
+    assert asp.device_status() == 0
+    live = torch.arange(T) < torch.tensor(lens)[:, None]
+    got = scores[:, 0].cpu()
+    assert torch.equal(torch.isnan(got), ~live)
+    for b in range(0, B, 97):
+        if lens[b]:
+            x, D = logit_bound(np64(q[b]), c.rows("k", b)[0])
+            check(np64(got[b, :lens[b]]), x.max(axis=0), D.max(axis=0), f"b{b}")
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_nan_and_infinite_queries_reach_the_scores(fmt):
+    """A head whose query is not finite gives scores that are not finite; its neighbours' stay."""
+    c = Cache(fmt, 1, 4, 128, 50, [50], 0, 16, seed=2)
+    q = torch.randn(1, 4, 128, generator=gen(5)).to(DEV)
+    clean = torch.empty(1, 4, 50, device=DEV)
+    asp.score_keys(q, c.kv, clean)
+    q[0, 1, 3], q[0, 2, 100] = float("nan"), float("inf")
+    scores = torch.empty(1, 4, 50, device=DEV)
+    asp.score_keys(q, c.kv, scores)
+    assert not torch.isfinite(scores[0, 1:3]).any()
+    assert torch.equal(scores[0, [0, 3]], clean[0, [0, 3]])
+
+
 # ---- attention and summed weights ---------------------------------------------------------------------------------------
 
 def selection(B, H, C, lens, tails, seed):
@@ -460,6 +493,42 @@ def test_a_uniform_long_tail_is_not_lost():
     v.copy_((torch.rand(v.shape, generator=gen(2)) + 1).to(torch.float8_e4m3fn))
     for dt in (torch.float32, torch.bfloat16):
         run_attention(c, q.to(dt), 0, "all", seed=1, accumulate=True)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8", "bf16"])
+def test_queries_off_the_16_byte_boundary(fmt):
+    """A query tensor that starts at an odd element is read correctly."""
+    c = Cache(fmt, 2, 2, 64, 700, [700, 9], 0, 16, seed=4)
+    for dt in (torch.bfloat16, torch.float32):
+        flat = torch.randn(2 * 8 * 64 + 1, generator=gen(5)).to(dt).to(DEV)
+        q = flat[1:].view(2, 8, 64)
+        assert q.data_ptr() % 16
+        run_attention(c, q, 0, "all", seed=1, accumulate=True)
+
+
+def test_many_captured_calls_back_to_back():
+    """Unsynchronised calls in a row over ragged lengths and units shared by CTAs: each waits for the one before."""
+    lens = [int(n) for n in np.random.default_rng(11).integers(1, 4000, 16)]
+    c = Cache("bf16", 16, 4, 128, 4000, lens, 0, 16, seed=3)
+    q = torch.randn(16, 16, 128, generator=gen(5)).to(torch.bfloat16).to(DEV)
+    tb = torch.zeros(16, dtype=torch.int32, device=DEV)
+    ws = torch.empty(asp.accumulate_workspace_bytes(c.kv, 16, 0, 4000), dtype=torch.uint8, device=DEV)
+    out, lse, acc = (torch.empty(16, 16, 128, dtype=torch.bfloat16, device=DEV), torch.empty(16, 16, device=DEV),
+                     torch.zeros(16, 4, 4000, device=DEV))
+    call = lambda: asp.attend_accumulate(q, c.kv, None, None, 0, out, acc, lse, tail_begin=tb, max_tail=4000, workspace=ws)
+    call()
+    torch.cuda.synchronize()
+    one, first = acc.clone(), out.clone()
+    acc.zero_()
+    for _ in range(40):
+        call()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first)
+    # 40 additions of the same value: at most 39 roundings of half a step of the largest sum
+    assert (acc - 40 * one).abs().max() <= 40 * 2.0 ** -24 * float(acc.max())
+    for b in range(16):
+        assert torch.allclose(one[b, :, :lens[b]].sum(-1), torch.full((4,), 4.0, device=DEV), rtol=1e-4)
+        assert (one[b, :, lens[b]:] == 0).all()
 
 
 def test_duplicate_free_selection_inside_the_tail_counts_once():
