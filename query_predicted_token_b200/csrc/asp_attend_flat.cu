@@ -534,12 +534,6 @@ __global__ void __launch_bounds__(kThreads, Fmt<CT>::kCtas) attend_flat_kernel(F
     const int seg_end = min(t1, seg_t0 + un);
     const int kend = seg_end - t0 - warp;
     const int jend = kend > 0 ? (kend + W - 1) / W : 0;
-    if (seg_end < t1) {      // the next unit's query towards L1
-      const int nb = (u + 1) / p.n_kv, nh = u + 1 - nb * p.n_kv;
-      const int es = p.q_f32 ? 4 : 2;
-      const uint8_t* const next = static_cast<const uint8_t*>(p.q) + ((size_t)nb * p.n_q_heads + nh * G) * D * es;
-      if (lane * 128 < G * D * es) asm volatile("prefetch.global.L1 [%0];" ::"l"(next + lane * 128));
-    }
     float o[MT][4];
 #pragma unroll
     for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;

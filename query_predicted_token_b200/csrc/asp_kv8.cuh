@@ -13,8 +13,6 @@
 namespace asp {
 
 struct CodeE4M3 {
-  // frexp mantissa of the largest code, 448 = 0.875 * 2^9: the fraction bits above
-  // which a value needs the next power of two, and the exponent it is taken off
   // packed magnitudes of four codes, and whether one of them is NaN
   __device__ __forceinline__ static uint32_t mag4(uint32_t w) { return w & 0x7f7f7f7fu; }
   static constexpr uint32_t kNanMag = 0x7fu;
@@ -33,6 +31,8 @@ struct CodeE4M3 {
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(*reinterpret_cast<const uint32_t*>(&y)));
     return (uint32_t)lo | ((uint32_t)hi << 16);
   }
+  // frexp mantissa of the largest code, 448 = 0.875 * 2^9: the fraction bits above
+  // which a value needs the next power of two, and the exponent it is taken off
   static constexpr uint32_t kTopFrac = 0x600000u;
   static constexpr int kShift = 9;
   // two codes (low, high byte) -> fp16x2 (low, high half), exact
