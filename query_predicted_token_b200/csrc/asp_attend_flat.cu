@@ -21,8 +21,10 @@
 //    byte permute from two rows' words, so V is not transposed through shared memory; P is, in
 //    registers, by movmatrix.  An fp32 query has a second fp16 part, one more product each.
 //  * K's scale multiplies the fp32 logits.  V's scale s = mant * 2^e multiplies the weight
-//    before it is rounded to fp16: w = 2^(x + e - M + 14) mant with M = ceil(max(x + e)),
-//    an integer like m, so rescaling is exact and no pair of scales leaves fp16's range.
+//    before it is rounded to fp16: w = 2^((x - m) + e - R + 14) mant with R = ceil(max((x - m) +
+//    e)).  Only R, m's distance from the maximum of x + e and so at most 127 either way, meets
+//    the exponents: they hold at any finite logit, whatever the spacing of floats there is.  m
+//    and R are integers, so rescaling is exact and no pair of scales leaves fp16's range.
 //    A weight keeps 11 bits (a second fp16 part, 22, for an fp32 query) down to 2^-28 of
 //    the largest.
 #include "asp_internal.h"
@@ -43,7 +45,8 @@ constexpr int kWBias = 14;      // the largest weight is below 2^15 before its r
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kNone = 0xffffffffu;
-constexpr float kLowest = -3e38f;   // a maximum before any row: finite, so that no difference is inf - inf
+constexpr float kLowest = -3.402823466e38f;   // a maximum before any row: finite, so that no difference is inf - inf
+constexpr float kNoRows = -1024.f;            // R before any row: below any row's
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -72,7 +75,7 @@ struct FlatParams {
   int max_tail;
   int whole;
   float* part_o;      // [2 ctas][G][d]
-  float* part_ml;     // [2 ctas][G][4]: m, l, M
+  float* part_ml;     // [2 ctas][G][4]: m, l, R
   int4* info;         // [units]: first CTA, last CTA, slot of the first
   float* stat;        // [units][G][2]: m, 1 / l of units one CTA holds (accumulate)
   float* logits;      // [units][G][row_stride] (accumulate)
@@ -538,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, Fmt<CT>::kCtas) attend_flat_kernel(F
 #pragma unroll
     for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     // of heads 2t and 2t + 1; l: this lane's share
-    float m[2] = {kLowest, kLowest}, M[2] = {kLowest, kLowest}, l[2] = {0.f, 0.f};
+    float m[2] = {kLowest, kLowest}, R[2] = {kNoRows, kNoRows}, l[2] = {0.f, 0.f};
 #pragma unroll 1
     for (; j < jend; ++j) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
@@ -607,23 +610,25 @@ __global__ void __launch_bounds__(kThreads, Fmt<CT>::kCtas) attend_flat_kernel(F
             lg[p.row_stride + 8] = x[3];
           }
         }
-        // a: exponents of the weights, at most 14 where M holds; the maxima are raised only
-        // when a row of the tile passes them
-        float a[4];
+        // dx: x - m; a: exponents of the weights, at most 14 where R holds; the maxima are raised
+        // only when a row of the tile passes them
+        float dx[4], a[4];
         const float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
         bool up = mx[0] > m[0] || mx[1] > m[1];
         auto exponents = [&]() {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float off = (float)kWBias - M[e];   // integers: exact
-            a[e] = x[e] + (ve[0] + off);
-            a[2 + e] = x[2 + e] + (ve[1] + off);
+          for (int e = 0; e < 4; ++e) dx[e] = x[e] - m[e & 1];
+          if constexpr (F::kScaled) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float off = (float)kWBias - R[e];   // integers below 2^12: exact
+              a[e] = dx[e] + (ve[0] + off);
+              a[2 + e] = dx[2 + e] + (ve[1] + off);
+            }
           }
         };
-        if constexpr (F::kScaled) {
-          exponents();
-          up |= fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) > (float)kWBias || M[0] == kLowest;
-        }
+        exponents();
+        if constexpr (F::kScaled) up |= fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) > (float)kWBias;
         if (__any_sync(0xffffffffu, up)) {
           float corr[2];
 #pragma unroll
@@ -633,20 +638,21 @@ __global__ void __launch_bounds__(kThreads, Fmt<CT>::kCtas) attend_flat_kernel(F
             mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, 8));
             mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, 16));
             const float mn = fmaxf(m[e], ceilf(mr));
-            corr[e] = ex2(m[e] - mn);
+            const float down = m[e] - mn;   // exact, or so far that what was there counts for nothing
+            corr[e] = ex2(down);
             l[e] *= corr[e];
             m[e] = mn;
             if constexpr (F::kScaled) {
-              float Mr = fmaxf(x[e] + ve[0], x[2 + e] + ve[1]);
-              Mr = fmaxf(Mr, __shfl_xor_sync(0xffffffffu, Mr, 4));
-              Mr = fmaxf(Mr, __shfl_xor_sync(0xffffffffu, Mr, 8));
-              Mr = fmaxf(Mr, __shfl_xor_sync(0xffffffffu, Mr, 16));
-              const float Mn = fmaxf(M[e], ceilf(Mr));
-              corr[e] = ex2(M[e] - Mn);
-              M[e] = Mn;
+              float Rr = fmaxf((x[e] - mn) + ve[0], (x[2 + e] - mn) + ve[1]);
+              Rr = fmaxf(Rr, __shfl_xor_sync(0xffffffffu, Rr, 4));
+              Rr = fmaxf(Rr, __shfl_xor_sync(0xffffffffu, Rr, 8));
+              Rr = fmaxf(Rr, __shfl_xor_sync(0xffffffffu, Rr, 16));
+              const float was = R[e] + down;   // R of the rows so far, from the new m
+              R[e] = fmaxf(fmaxf(was, ceilf(Rr)), kNoRows);
+              corr[e] = ex2(was - R[e]);
             }
           }
-          if constexpr (F::kScaled) exponents();
+          exponents();
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
             o[i][0] *= corr[0];
@@ -657,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, Fmt<CT>::kCtas) attend_flat_kernel(F
         }
         float w4[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w4[e] = ex2(x[e] - m[e & 1]);
+        for (int e = 0; e < 4; ++e) w4[e] = ex2(dx[e]);
         l[0] += w4[0] + w4[2];
         l[1] += w4[1] + w4[3];
         if constexpr (F::kScaled) {
@@ -727,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, Fmt<CT>::kCtas) attend_flat_kernel(F
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
-      if constexpr (!F::kScaled) M[e] = m[e];
+      if constexpr (!F::kScaled) R[e] = 0.f;
     }
 
     // ---- the warps' results of this unit meet in shared memory (position 16 i + 2 g + e of a
@@ -741,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, Fmt<CT>::kCtas) attend_flat_kernel(F
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         if (2 * t + e < G)
-          *reinterpret_cast<float4*>(mml + (warp * G + 2 * t + e) * 4) = make_float4(m[e], l[e], M[e], 0.f);
+          *reinterpret_cast<float4*>(mml + (warp * G + 2 * t + e) * 4) = make_float4(m[e], l[e], R[e], 0.f);
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -766,17 +772,18 @@ __global__ void __launch_bounds__(kThreads, Fmt<CT>::kCtas) attend_flat_kernel(F
       for (int gg = 0; gg < G; ++gg) {
         // lane w: warp w's statistics of the head and the factor of its output (l = 0, o = 0
         // for a warp without rows)
-        float4 ml = make_float4(kLowest, 0.f, kLowest, 0.f);
+        float4 ml = make_float4(kLowest, 0.f, kNoRows, 0.f);
         if (lane < W) ml = *reinterpret_cast<const float4*>(mml + (lane * G + gg) * 4);
-        float mm = ml.x, MM = ml.z;
+        float mm = ml.x;
 #pragma unroll
-        for (int sh = W / 2; sh; sh >>= 1) {
-          mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, sh));
-          MM = fmaxf(MM, __shfl_xor_sync(0xffffffffu, MM, sh));
-        }
+        for (int sh = W / 2; sh; sh >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, sh));
         mm = __shfl_sync(0xffffffffu, mm, 0);
-        MM = __shfl_sync(0xffffffffu, MM, 0);
-        const float fw = ex2(ml.z - MM);
+        const float rw = ml.z + (ml.x - mm);   // the warp's R from the common m
+        float RR = fmaxf(rw, kNoRows);
+#pragma unroll
+        for (int sh = W / 2; sh; sh >>= 1) RR = fmaxf(RR, __shfl_xor_sync(0xffffffffu, RR, sh));
+        RR = __shfl_sync(0xffffffffu, RR, 0);
+        const float fw = ex2(rw - RR);
         float L = ml.y * ex2(ml.x - mm);
 #pragma unroll
         for (int sh = W / 2; sh; sh >>= 1) L += __shfl_xor_sync(0xffffffffu, L, sh);
@@ -784,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, Fmt<CT>::kCtas) attend_flat_kernel(F
         float f[W];
 #pragma unroll
         for (int w = 0; w < W; ++w) f[w] = __shfl_sync(0xffffffffu, fw, w);
-        const float scale = L == 0.f ? 0.f : ex2(MM - mm - (F::kScaled ? (float)kWBias : 0.f)) / L;
+        const float scale = L == 0.f ? 0.f : ex2(RR - (F::kScaled ? (float)kWBias : 0.f)) / L;
         const size_t bh = (size_t)b * p.n_q_heads + h * G + gg;
 #pragma unroll
         for (int k = 0; k < D / 64; ++k) {   // two channels per lane
@@ -813,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, Fmt<CT>::kCtas) attend_flat_kernel(F
         }
         if (lane == 0) {
           if (!alone) {
-            *reinterpret_cast<float4*>(p.part_ml + ((size_t)slot * G + gg) * 4) = make_float4(mm, L, MM, 0.f);
+            *reinterpret_cast<float4*>(p.part_ml + ((size_t)slot * G + gg) * 4) = make_float4(mm, L, RR, 0.f);
           } else {
             if (p.lse) p.lse[bh] = L == 0.f ? -INFINITY : mm * kLn2 + logf(L);
             if constexpr (ACC) {
@@ -850,8 +857,8 @@ __global__ void __launch_bounds__(kThreads, Fmt<CT>::kCtas) attend_flat_kernel(F
 // of the unit's rows (blockIdx.y: chunks of kAccRows rows).
 template <int D, bool ACC>
 __global__ void __launch_bounds__(kFinThreads) finish_kernel(FlatParams p, float bias) {
-  __shared__ float fac[8][kMaxCtas];       // weight of a CTA's output
-  __shared__ float s_m[8], s_l[8], s_M[8];
+  __shared__ float2 fac[8][kMaxCtas];      // of a CTA's output: its m and R, then its weight
+  __shared__ float s_m[8], s_l[8], s_R[8];
   __shared__ float4 red[kFinThreads];
   const int u = blockIdx.x, G = p.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
@@ -869,28 +876,33 @@ __global__ void __launch_bounds__(kFinThreads) finish_kernel(FlatParams p, float
   auto slot_of = [&](int i) -> int { return i == 0 ? in.z : 2 * (in.x + i); };
   if (warp < G) {   // warp gg: statistics of head gg
     if (n > 1) {
-      float mm = kLowest, MM = kLowest, L = 0.f;
+      float mm = kLowest, RR = kNoRows, L = 0.f;
       for (int i = lane; i < n; i += 32) {
         const float4 ml = *reinterpret_cast<const float4*>(p.part_ml + ((size_t)slot_of(i) * G + warp) * 4);
-        fac[warp][i] = ml.z;
-        MM = fmaxf(MM, ml.z);
+        fac[warp][i] = make_float2(ml.x, ml.z);
         const float mn = fmaxf(mm, ml.x);
         L = L * ex2(mm - mn) + ml.y * ex2(ml.x - mn);
         mm = mn;
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) {
-        MM = fmaxf(MM, __shfl_xor_sync(0xffffffffu, MM, o));
         const float m2 = __shfl_xor_sync(0xffffffffu, mm, o), l2 = __shfl_xor_sync(0xffffffffu, L, o);
         const float mn = fmaxf(mm, m2);
         L = L * ex2(mm - mn) + l2 * ex2(m2 - mn);
         mm = mn;
       }
-      for (int i = lane; i < n; i += 32) fac[warp][i] = ex2(fac[warp][i] - MM);
+      for (int i = lane; i < n; i += 32) {   // R from the common m
+        const float2 f = fac[warp][i];
+        fac[warp][i].x = f.y + (f.x - mm);
+        RR = fmaxf(RR, fac[warp][i].x);
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) RR = fmaxf(RR, __shfl_xor_sync(0xffffffffu, RR, o));
+      for (int i = lane; i < n; i += 32) fac[warp][i].x = ex2(fac[warp][i].x - RR);
       if (lane == 0) {
         s_m[warp] = mm;
         s_l[warp] = L;
-        s_M[warp] = MM;
+        s_R[warp] = RR;
       }
     } else if (lane == 0) {
       s_m[warp] = p.stat[((size_t)u * G + warp) * 2];
@@ -906,7 +918,7 @@ __global__ void __launch_bounds__(kFinThreads) finish_kernel(FlatParams p, float
 #pragma unroll 4
     for (int i = grp; i < n; i += ngrp) {
       const float4 x = *reinterpret_cast<const float4*>(p.part_o + ((size_t)slot_of(i) * G + gg) * D + c);
-      const float f = fac[gg][i];
+      const float f = fac[gg][i].x;
       a.x += x.x * f;
       a.y += x.y * f;
       a.z += x.z * f;
@@ -925,7 +937,7 @@ __global__ void __launch_bounds__(kFinThreads) finish_kernel(FlatParams p, float
       const int b = u / p.n_kv, h = u - b * p.n_kv;
       const size_t bh = (size_t)b * p.n_q_heads + h * G + gg;
       const float L = s_l[gg], mm = s_m[gg];
-      const float f = ex2(s_M[gg] - mm - bias);
+      const float f = ex2(s_R[gg] - bias);
       const float y[4] = {a.x / L * f, a.y / L * f, a.z / L * f, a.w / L * f};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
