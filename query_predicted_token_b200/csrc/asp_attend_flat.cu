@@ -220,14 +220,25 @@ __device__ __forceinline__ void load_logits(const FlatParams& p, int u, const Un
           (reinterpret_cast<uintptr_t>(p.acc + (size_t)u * p.t_max + q.tok[0]) & 15) == 0;
 }
 
-// acc of those rows: the weights of the group's heads, each from its logit by `weight`.
+// acc of those rows: the weights of the group's heads, each from its logit by `weight`.  A row
+// whose logits are -inf in every head was not attended (or has no weight); one head's can overflow
+// to it alone.
 template <typename W>
 __device__ __forceinline__ void add_weights(const FlatParams& p, int u, const RowLogits& q, W weight) {
   float w[4] = {0.f, 0.f, 0.f, 0.f};
   bool has[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    has[k] = q.tok[k] >= 0 && (k == 0 ? q.x[0].x : k == 1 ? q.x[0].y : k == 2 ? q.x[0].z : q.x[0].w) != -INFINITY;
+  for (int k = 0; k < 4; ++k) has[k] = false;
+#pragma unroll
+  for (int gg = 0; gg < 8; ++gg)
+    if (gg < p.G) {
+      has[0] |= q.x[gg].x != -INFINITY;
+      has[1] |= q.x[gg].y != -INFINITY;
+      has[2] |= q.x[gg].z != -INFINITY;
+      has[3] |= q.x[gg].w != -INFINITY;
+    }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) has[k] &= q.tok[k] >= 0;
   if (!(has[0] || has[1] || has[2] || has[3])) return;
 #pragma unroll
   for (int gg = 0; gg < 8; ++gg)
@@ -837,10 +848,15 @@ __global__ void __launch_bounds__(kThreads, Fmt<CT>::kCtas) attend_flat_kernel(F
         const float* const stat = p.stat + (size_t)u * G * 2;
         for (int r = threadIdx.x; r < ur.n_rows; r += THREADS) {   // few rows: one at a time, in few registers
           const float* const x = p.logits + (size_t)u * G * p.row_stride + r;
-          if (x[0] == -INFINITY) continue;
           float w = 0.f;
+          bool has = false;        // as in add_weights
 #pragma unroll 1
-          for (int gg = 0; gg < G; ++gg) w += ex2(x[(size_t)gg * p.row_stride] - stat[2 * gg]) * stat[2 * gg + 1];
+          for (int gg = 0; gg < G; ++gg) {
+            const float xv = x[(size_t)gg * p.row_stride];
+            has |= xv != -INFINITY;
+            w += ex2(xv - stat[2 * gg]) * stat[2 * gg + 1];
+          }
+          if (!has) continue;
           const int tok = r < ur.n_sel ? p.idx[(size_t)u * p.C + r] : ur.tb + (r - ur.n_sel);
           atomicAdd(p.acc + (size_t)u * p.t_max + tok, w);
         }

@@ -13,7 +13,7 @@ import torch
 
 import query_predicted_token_b200 as asp
 from parity_util import np64
-from test_gpu_cache8 import CODE, DEV, WIDE, Cache, _built, check, logit_bound  # noqa: F401
+from test_gpu_cache8 import CODE, DEV, WIDE, Cache, _built, attend_ref, check, gen, logit_bound  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -106,3 +106,37 @@ def test_large_logits_bf16_cache(qd, T):
     for i, logit in enumerate(LOGITS):
         c, q, lens = uniform_case("bf16", qd, T, logit, seed=T + i)
         check_uniform(c, q, lens, T, True)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8", "bf16", "f32"])
+@pytest.mark.parametrize("T", [40, 500, 900])
+@pytest.mark.parametrize("G", [2, 8])
+def test_sums_where_one_heads_logit_overflows(fmt, T, G):
+    """Head 0's logit of one row is -inf: the other heads' weights of that row still count."""
+    c = Cache(fmt, 1, 1, 64, T, [T], 0, 16, seed=T)
+    k, ks = c.side["k"]
+    if ks is not None:
+        ks.fill_(2.0 ** -6)
+    k[..., 0] = 0
+    r = T - 7
+    k[0, 0, r, 0] = 64.0 if fmt in CODE else 1.0
+    if ks is not None:
+        ks[0, 0, r // 16] = 1.0
+    K = c.rows("k", 0)[0]
+    q = torch.randn(1, G, 64, generator=gen(5))
+    q[..., 0] = 0
+    q[0, 0] = 0
+    q[0, 0, 0] = -1.9375 * 2.0 ** 127      # one part in bf16 and fp16
+    if fmt not in CODE:        # a wide cache's keys are not scaled: one of 2^12 overflows
+        k[0, 0, r, 0] = 2.0 ** 12
+        K = c.rows("k", 0)[0]
+    out = torch.empty(1, G, 64, dtype=torch.float32 if fmt != "bf16" else torch.bfloat16, device=DEV)
+    lse, acc = torch.empty(1, G, device=DEV), torch.zeros(1, 1, T, device=DEV)
+    tb = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = torch.empty(asp.accumulate_workspace_bytes(c.kv, G, 0, T), dtype=torch.uint8, device=DEV)
+    asp.attend_accumulate(q.to(DEV), c.kv, None, None, 0, out, acc, lse, tail_begin=tb, max_tail=T, workspace=ws)
+    _, _, _, _, w, wb = attend_ref(np64(q[0, 1:]), K, c.rows("v", 0)[0], np.arange(T), False, 2.0 ** -8)
+    w0 = np.full(T, 1 / (T - 1))      # head 0: equal logits on the other rows
+    w0[r] = 0
+    check(np64(acc[0, 0]), w + w0, wb + w0 * (2.0 ** -19 + T / 16 * 2.0 ** -23) + 2.0 ** -23 * (w + w0), "acc")
+    assert np.isfinite(np64(lse)).all()
