@@ -170,18 +170,18 @@ bool sizes_ok(const asp_kv* kv, int n_q_heads, int C, int max_tail) {
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Workspace of asp_attend_accumulate for an fp32 cache: the attention's partials, the lse,
-// the logits.
+// Workspace of asp_attend_accumulate for an fp32 cache: the attention's partials, each head's
+// maximum and 1 / sum, the logits.
 struct WideAccumulate {
-  size_t lse_off, logits_off, bytes;
+  size_t stat_off, logits_off, bytes;
   int row_stride;
 };
 WideAccumulate wide_accumulate(const asp_kv* kv, int n_q_heads, int C, int mt, size_t partials) {
   WideAccumulate w;
   const size_t heads = (size_t)kv->batch * n_q_heads;
   w.row_stride = (int)(((long)C + mt + 15) / 16 * 16);
-  w.lse_off = round256(partials);
-  w.logits_off = w.lse_off + round256(heads * 4);
+  w.stat_off = round256(partials);
+  w.logits_off = w.stat_off + round256(heads * 8);
   w.bytes = w.logits_off + round256(heads * w.row_stride * 4);
   return w;
 }
@@ -453,12 +453,12 @@ asp_status asp_attend_accumulate(const void* q, asp_dtype q_dtype, int n_q_heads
                                                flat_plan_of(kv, n_q_heads, C, mt, true, 0), s));
   const WideAccumulate w = wide_accumulate(kv, n_q_heads, C, mt, plan.workspace_bytes);
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
-  if (!lse) lse = reinterpret_cast<float*>(ws + w.lse_off);
+  float* const stat = reinterpret_cast<float*>(ws + w.stat_off);
   float* const logits = reinterpret_cast<float*>(ws + w.logits_off);
   cudaError_t e = asp::launch_attend_logits(q, q_dtype == ASP_F32, n_q_heads, v, idx, count, C, tail_begin, max_tail,
-                                            out, lse, ws, plan, logits, w.row_stride, s);
+                                            out, lse, ws, plan, logits, w.row_stride, stat, s);
   if (e == cudaSuccess)
-    e = asp::launch_accumulate(logits, w.row_stride, lse, n_q_heads, v, idx, count, C, tail_begin, max_tail, acc, s);
+    e = asp::launch_accumulate(logits, w.row_stride, stat, n_q_heads, v, idx, count, C, tail_begin, max_tail, acc, s);
   return cuda_status(e);
 }
 

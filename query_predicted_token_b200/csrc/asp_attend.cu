@@ -64,9 +64,17 @@ struct AttParams {
   float qscale;   // log2(e) / sqrt(d)
   float* logits;  // attend_kernel with LOGITS: [units][G][logits_stride], base 2
   int logits_stride;
+  float* stat;    // with LOGITS: [units][G][2], the logits' maximum and 1 / sum 2^(x - maximum)
 };
 
-// LOGITS: every row's logits are also left in p.logits (-inf for rows not attended).
+// A head without rows, or whose weights are all zero, gives none: any finite maximum will do.
+__device__ __forceinline__ void write_stat(float* stat, float M, float L) {
+  stat[0] = M == -INFINITY ? 0.f : M;
+  stat[1] = L == 0.f ? 0.f : 1.f / L;
+}
+
+// LOGITS: every row's logits are also left in p.logits (-inf for rows not attended), and each
+// head's maximum and 1 / sum in p.stat.
 template <typename KT, int D, int G, int STAGES, bool LOGITS = false>
 __global__ void __launch_bounds__(kWarps * 32) attend_kernel(AttParams p) {
   using E = Elem<KT>;
@@ -396,6 +404,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(AttParams p) {
       const float r = L > 0.f ? O / L : 0.f;
       static_cast<KT*>(p.out)[bh * D + c] = E::from_float(r);
       if (c == 0 && p.lse) p.lse[bh] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+      if (LOGITS && c == 0) write_stat(p.stat + 2 * bh, M, L);
     } else {
       p.part_o[(bh * p.splits + split) * D + c] = O;
       if (c == 0) {
@@ -1291,10 +1300,11 @@ __global__ void __launch_bounds__(D) attend_gather_merge_kernel(AttParams p, int
 }
 
 // Log-sum-exp merge of the split partials: one CTA of D threads per query head.
-template <typename KT, int D>
+// STAT: each head's maximum and 1 / sum are left in stat.
+template <typename KT, int D, bool STAT = false>
 __global__ void __launch_bounds__(D) attend_merge_kernel(const float* __restrict__ part_o,
                                                          const float* __restrict__ part_ml, int splits, void* out,
-                                                         float* lse) {
+                                                         float* lse, float* stat) {
   using E = Elem<KT>;
   const size_t bh = blockIdx.x;
   const int c = threadIdx.x;
@@ -1315,6 +1325,7 @@ __global__ void __launch_bounds__(D) attend_merge_kernel(const float* __restrict
   }
   static_cast<KT*>(out)[bh * D + c] = E::from_float(L > 0.f ? O / L : 0.f);
   if (c == 0 && lse) lse[bh] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+  if (STAT && c == 0) write_stat(stat + 2 * bh, M, L);
 }
 
 template <typename KT, int D, int G, bool LOGITS = false>
@@ -1330,8 +1341,8 @@ cudaError_t launch_t(const AttParams& p, cudaStream_t s) {
   kern<<<dim3(p.splits, p.batch * p.n_kv), kWarps * 32, smem, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.splits == 1) return e;
-  return launch_pdl(attend_merge_kernel<KT, D>, dim3(p.batch * p.n_q_heads), dim3(D), 0, s, (const float*)p.part_o,
-                    (const float*)p.part_ml, p.splits, p.out, p.lse);
+  return launch_pdl(attend_merge_kernel<KT, D, LOGITS>, dim3(p.batch * p.n_q_heads), dim3(D), 0, s,
+                    (const float*)p.part_o, (const float*)p.part_ml, p.splits, p.out, p.lse, p.stat);
 }
 
 template <int D, int G>
@@ -1358,7 +1369,7 @@ cudaError_t launch_mma(const AttParams& p, cudaStream_t s) {
   cudaError_t e = launch_pdl(kern, dim3(p.ctas), dim3(kWarps * 32), smem, s, p);
   if (e != cudaSuccess || p.splits == 1) return e;
   return launch_pdl(attend_merge_kernel<__nv_bfloat16, D>, dim3(p.batch * p.n_q_heads), dim3(D), 0, s,
-                    (const float*)p.part_o, (const float*)p.part_ml, p.splits, p.out, p.lse);
+                    (const float*)p.part_o, (const float*)p.part_ml, p.splits, p.out, p.lse, p.stat);
 }
 
 template <int D>
@@ -1518,7 +1529,7 @@ static AttParams attend_params(const void* q, int q_f32, int n_q_heads, const Kv
                                const int32_t* count, int C, const int32_t* tail_begin, int max_tail, void* out,
                                float* lse, void* workspace, const AttendPlan& plan, bool gather) {
   AttParams p;
-  p.logits = nullptr;
+  p.logits = p.stat = nullptr;
   p.logits_stride = 0;
   p.q = q;
   p.q_f32 = q_f32;
@@ -1582,11 +1593,12 @@ cudaError_t launch_attend(const void* q, int q_f32, int n_q_heads, const KvView&
 cudaError_t launch_attend_logits(const void* q, int q_f32, int n_q_heads, const KvView& kv, const int32_t* idx,
                                  const int32_t* count, int C, const int32_t* tail_begin, int max_tail, void* out,
                                  float* lse, void* workspace, const AttendPlan& plan, float* logits, int row_stride,
-                                 cudaStream_t s) {
+                                 float* stat, cudaStream_t s) {
   AttParams p = attend_params(q, q_f32, n_q_heads, kv, idx, count, C, tail_begin, max_tail, out, lse, workspace, plan,
                               false);
   p.logits = logits;
   p.logits_stride = row_stride;
+  p.stat = stat;
   const int G = n_q_heads / kv.n_kv;
   return kv.head_dim == 64 ? dispatch_g<float, 64, true>(G, p, s) : dispatch_g<float, 128, true>(G, p, s);
 }

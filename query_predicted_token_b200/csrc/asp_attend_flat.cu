@@ -77,7 +77,7 @@ struct FlatParams {
   float* part_o;      // [2 ctas][G][d]
   float* part_ml;     // [2 ctas][G][4]: m, l, R
   int4* info;         // [units]: first CTA, last CTA, slot of the first
-  float* stat;        // [units][G][2]: m, 1 / l of units one CTA holds (accumulate)
+  float* stat;        // [units][G][2]: m, 1 / l (accumulate; of attend_flat_kernel, where one CTA holds the unit)
   float* logits;      // [units][G][row_stride] (accumulate)
   int row_stride;
   float* acc;
@@ -972,19 +972,23 @@ __global__ void __launch_bounds__(kFinThreads) finish_kernel(FlatParams p, float
   }
 }
 
-// acc from the logits (base 2) of attend_kernel and the final lse.
+// acc from the logits (base 2) and statistics of attend_kernel: the weights come from x - m as
+// the output's do, so that they sum to the group's heads at any size of the logits (from the
+// lse, a rounded sum of logit and logarithm, they would be off by |lse| 2^-24 relative).
 __global__ void __launch_bounds__(kFinThreads) accumulate_kernel(FlatParams p) {
-  __shared__ float s_l[8];
+  __shared__ float s_m[8], s_l[8];
   const int u = blockIdx.x, G = p.G;
-  const int b = u / p.n_kv, h = u - b * p.n_kv;
   pdl_wait();
   const UnitRows ur = unit_rows(p, u, false);
   if ((int)blockIdx.y * kAccRows >= ur.n_rows) return;
   RowLogits rows;
   load_logits(p, u, ur, blockIdx.y * kAccRows + 4 * threadIdx.x, rows);
-  if (threadIdx.x < G) s_l[threadIdx.x] = p.lse[(size_t)b * p.n_q_heads + h * G + threadIdx.x];
+  if (threadIdx.x < G) {
+    s_m[threadIdx.x] = p.stat[((size_t)u * G + threadIdx.x) * 2];
+    s_l[threadIdx.x] = p.stat[((size_t)u * G + threadIdx.x) * 2 + 1];
+  }
   __syncthreads();
-  add_weights(p, u, rows, [&](int gg, float xv) { return expf(xv * kLn2 - s_l[gg]); });
+  add_weights(p, u, rows, [&](int gg, float xv) { return ex2(xv - s_m[gg]) * s_l[gg]; });
 }
 
 template <typename CT, int D, int QP, bool ACC>
@@ -1103,13 +1107,13 @@ cudaError_t launch_attend_flat(const void* q, int q_f32, int n_q_heads, const Kv
                : launch_flat_d<__nv_bfloat16, 1, true>(p, kv.head_dim, pl.ctas, chunks, s);
 }
 
-cudaError_t launch_accumulate(const float* logits, int row_stride, const float* lse, int n_q_heads, const KvView& kv,
+cudaError_t launch_accumulate(const float* logits, int row_stride, const float* stat, int n_q_heads, const KvView& kv,
                               const int32_t* idx, const int32_t* count, int C, const int32_t* tail_begin, int max_tail,
                               float* acc, cudaStream_t s) {
   FlatParams p = flat_params(nullptr, 1, n_q_heads, kv, idx, count, C, tail_begin, max_tail);
   p.logits = const_cast<float*>(logits);
   p.row_stride = row_stride;
-  p.lse = const_cast<float*>(lse);
+  p.stat = const_cast<float*>(stat);
   p.acc = acc;
   return launch_pdl(accumulate_kernel, dim3(p.units, (row_stride + kAccRows - 1) / kAccRows), dim3(kFinThreads), 0, s, p);
 }

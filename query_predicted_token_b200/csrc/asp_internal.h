@@ -231,11 +231,12 @@ cudaError_t launch_attend(const void* q, int q_f32, int n_q_heads, const KvView&
                           const int32_t* count, int C, const int32_t* tail_begin, int max_tail, void* out,
                           float* lse, void* workspace, const AttendPlan& plan, cudaStream_t s);
 // The same for an fp32 cache (plan made with ctas_per_sm 0), leaving the logits (base 2;
-// -inf for rows not attended) in logits [batch * n_kv, G, row_stride].
+// -inf for rows not attended) in logits [batch * n_kv, G, row_stride], and each head's maximum
+// and 1 / sum 2^(logit - maximum) in stat [batch * n_kv, G, 2].
 cudaError_t launch_attend_logits(const void* q, int q_f32, int n_q_heads, const KvView& kv, const int32_t* idx,
                                  const int32_t* count, int C, const int32_t* tail_begin, int max_tail, void* out,
                                  float* lse, void* workspace, const AttendPlan& plan, float* logits, int row_stride,
-                                 cudaStream_t s);
+                                 float* stat, cudaStream_t s);
 
 // Launches step 4 with its split-K partials in the library's fixed scratch array
 // (asp_sparse_attend_noalloc); `plan.workspace_bytes` must fit in it.
@@ -259,8 +260,8 @@ FlatPlan flat_plan(int batch, int n_q_heads, int n_kv_heads, int head_dim, int C
 cudaError_t launch_attend_flat(const void* q, int q_f32, int n_q_heads, const KvView& kv, const int32_t* idx,
                                const int32_t* count, int C, const int32_t* tail_begin, int max_tail, void* out,
                                float* lse, float* acc, void* workspace, const FlatPlan& plan, cudaStream_t s);
-// acc of an fp32 cache from the logits that attend_kernel left and the final lse.
-cudaError_t launch_accumulate(const float* logits, int row_stride, const float* lse, int n_q_heads, const KvView& kv,
+// acc of an fp32 cache from the logits and statistics that attend_kernel left.
+cudaError_t launch_accumulate(const float* logits, int row_stride, const float* stat, int n_q_heads, const KvView& kv,
                               const int32_t* idx, const int32_t* count, int C, const int32_t* tail_begin, int max_tail,
                               float* acc, cudaStream_t s);
 

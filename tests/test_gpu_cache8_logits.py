@@ -108,6 +108,14 @@ def test_large_logits_bf16_cache(qd, T):
         check_uniform(c, q, lens, T, True)
 
 
+@pytest.mark.parametrize("qd", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 40, 700])
+def test_large_logits_fp32_cache(qd, T):
+    for i, logit in enumerate(LOGITS):
+        c, q, lens = uniform_case("f32", qd, T, logit, seed=T + i)
+        check_uniform(c, q, lens, T, True)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8", "bf16", "f32"])
 @pytest.mark.parametrize("T", [40, 500, 900])
 @pytest.mark.parametrize("G", [2, 8])
