@@ -188,7 +188,8 @@ ASP_API asp_status asp_predict_query(float* qhist, int ring_start, const void* q
  * Entries j >= T_b of a row are not written.  fp32 arithmetic.  8-bit caches: k is
  * code * scale; the query enters as 22 bits of each head's largest channel (two fp16 parts,
  * or three 8-bit digits for ASP_I8), its products with the codes are exact, and the scale
- * multiplies their sum.
+ * multiplies their sum; a head of qpred that holds a NaN or an infinity gives NaN scores to
+ * its group.
  * qpred  : device fp32 [batch, n_q_heads, head_dim].
  * scores : device fp32 [batch, n_kv_heads, t_max], written.
  * Errors: ASP_ERR_INVALID_ARG; ASP_ERR_UNSUPPORTED (G not in {1,2,4,8}, head_dim

@@ -84,6 +84,14 @@ __device__ __forceinline__ void mma_s8_0(int (&c)[4], uint32_t a0, uint32_t a1, 
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
 }
 
+// Maximum that keeps a NaN (fmaxf drops it): a head that is not finite must not vanish behind its
+// group's others.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // The query is read twice, for its largest channel and for its parts, so that only one piece of
 // it is in registers at a time beside the rows in flight.
 __device__ __forceinline__ void ld_query(const float* p, float (&x)[4]) {
@@ -178,7 +186,7 @@ struct Query<CodeE4M3, D, NT> {   // NT = 1 for up to 4 heads, 2 for 8; column g
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         best[u][e] = t < p.G ? (acc[u][0][2 * e] + acc[u][0][2 * e + 1]) * fac[0] : -INFINITY;
-        if constexpr (NT == 2) best[u][e] = fmaxf(best[u][e], (acc[u][1][2 * e] + acc[u][1][2 * e + 1]) * fac[1]);
+        if constexpr (NT == 2) best[u][e] = max_nan(best[u][e], (acc[u][1][2 * e] + acc[u][1][2 * e + 1]) * fac[1]);
       }
   }
 };
@@ -258,7 +266,7 @@ struct Query<CodeI8, D, NT> {     // NT = 3: column g of n-tile n is digit n (hi
         for (int c = 0; c < 2; ++c)
           v[c] = fmaf((float)acc[u][0][2 * e + c], 65536.f,
                       (float)(acc[u][1][2 * e + c] * 256 + acc[u][2][2 * e + c])) * fac[c];
-        best[u][e] = 2 * t + 1 < p.G ? fmaxf(v[0], v[1]) : (2 * t < p.G ? v[0] : -INFINITY);
+        best[u][e] = 2 * t + 1 < p.G ? max_nan(v[0], v[1]) : (2 * t < p.G ? v[0] : -INFINITY);
       }
   }
 };
@@ -450,9 +458,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) score8_kernel(Score8Params p) 
       // maximum over the four lanes of a row: each lane ends with one of the four rows
       const bool up2 = t & 2, up1 = t & 1;
       float v0 = up2 ? best[u + 1][0] : best[u][0], v1 = up2 ? best[u + 1][1] : best[u][1];
-      v0 = fmaxf(v0, __shfl_xor_sync(0xffffffffu, up2 ? best[u][0] : best[u + 1][0], 2));
-      v1 = fmaxf(v1, __shfl_xor_sync(0xffffffffu, up2 ? best[u][1] : best[u + 1][1], 2));
-      const float m = fmaxf(up1 ? v1 : v0, __shfl_xor_sync(0xffffffffu, up1 ? v0 : v1, 1)) * scale[u / 2];
+      v0 = max_nan(v0, __shfl_xor_sync(0xffffffffu, up2 ? best[u][0] : best[u + 1][0], 2));
+      v1 = max_nan(v1, __shfl_xor_sync(0xffffffffu, up2 ? best[u][1] : best[u + 1][1], 2));
+      const float m = max_nan(up1 ? v1 : v0, __shfl_xor_sync(0xffffffffu, up1 ? v0 : v1, 1)) * scale[u / 2];
       const int j = cc.blk * kRows + 16 * u + (t >> 1) * 16 + (t & 1) * 8 + g;
       const bool has = j < cc.T;
       if (has) p.scores[row * p.t_max + j] = m;
