@@ -227,19 +227,21 @@ template <typename W>
 __device__ __forceinline__ void add_weights(const FlatParams& p, int u, const RowLogits& q, W weight) {
   float w[4] = {0.f, 0.f, 0.f, 0.f};
   bool has[4];
+  if (q.tok[0] < 0) return;              // past the unit's rows
 #pragma unroll
-  for (int k = 0; k < 4; ++k) has[k] = false;
+  for (int k = 0; k < 4; ++k) has[k] = (k == 0 ? q.x[0].x : k == 1 ? q.x[0].y : k == 2 ? q.x[0].z : q.x[0].w) != -INFINITY;
+  if (!(has[0] && has[1] && has[2] && has[3])) {   // rare: the other heads
 #pragma unroll
-  for (int gg = 0; gg < 8; ++gg)
-    if (gg < p.G) {
-      has[0] |= q.x[gg].x != -INFINITY;
-      has[1] |= q.x[gg].y != -INFINITY;
-      has[2] |= q.x[gg].z != -INFINITY;
-      has[3] |= q.x[gg].w != -INFINITY;
-    }
+    for (int gg = 1; gg < 8; ++gg)
+      if (gg < p.G) {
+        has[0] |= q.x[gg].x != -INFINITY;
+        has[1] |= q.x[gg].y != -INFINITY;
+        has[2] |= q.x[gg].z != -INFINITY;
+        has[3] |= q.x[gg].w != -INFINITY;
+      }
+  }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) has[k] &= q.tok[k] >= 0;
-  if (!(has[0] || has[1] || has[2] || has[3])) return;
+  for (int k = 0; k < 4; ++k) has[k] = has[k] && q.tok[k] >= 0;
 #pragma unroll
   for (int gg = 0; gg < 8; ++gg)
     if (gg < p.G) {
@@ -897,24 +899,24 @@ __global__ void __launch_bounds__(kFinThreads) finish_kernel(FlatParams p, float
         const float4 ml = *reinterpret_cast<const float4*>(p.part_ml + ((size_t)slot_of(i) * G + warp) * 4);
         fac[warp][i] = make_float2(ml.x, ml.z);
         const float mn = fmaxf(mm, ml.x);
+        RR = fmaxf(RR + (mm - mn), ml.z + (ml.x - mn));
         L = L * ex2(mm - mn) + ml.y * ex2(ml.x - mn);
         mm = mn;
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) {
         const float m2 = __shfl_xor_sync(0xffffffffu, mm, o), l2 = __shfl_xor_sync(0xffffffffu, L, o);
+        const float r2 = __shfl_xor_sync(0xffffffffu, RR, o);
         const float mn = fmaxf(mm, m2);
+        RR = fmaxf(RR + (mm - mn), r2 + (m2 - mn));
         L = L * ex2(mm - mn) + l2 * ex2(m2 - mn);
         mm = mn;
       }
-      for (int i = lane; i < n; i += 32) {   // R from the common m
+      RR = fmaxf(RR, kNoRows);
+      for (int i = lane; i < n; i += 32) {
         const float2 f = fac[warp][i];
-        fac[warp][i].x = f.y + (f.x - mm);
-        RR = fmaxf(RR, fac[warp][i].x);
+        fac[warp][i].x = ex2((f.y + (f.x - mm)) - RR);
       }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) RR = fmaxf(RR, __shfl_xor_sync(0xffffffffu, RR, o));
-      for (int i = lane; i < n; i += 32) fac[warp][i].x = ex2(fac[warp][i].x - RR);
       if (lane == 0) {
         s_m[warp] = mm;
         s_l[warp] = L;
