@@ -6,8 +6,9 @@ C1  scale of a block: the smallest power of two s >= 2^-100 with max |x| <= qmax
     block's finite values (qmax 448 for E4M3, 127 for 8-bit integers).
 C2  code of x: x / s rounded to the nearest representable value, ties to even; infinities
     become +-qmax, NaN stays NaN (E4M3) or becomes 0 (integers).
-C3  append: a token that opens a block sets its scale by C1; a later one raises it to what it
-    needs, and the older codes of the block are rounded again at the new scale.
+C3  append: a token that opens a block sets its scale by C1; a later one that does not fit (max |x|
+    > qmax s over its finite values) raises it to what it needs by C1, and the older codes of the
+    block are rounded again at the new scale.
 C4  summed weights: acc_j += sum over the group's query heads of softmax_j over the attended
     set.
 C5  eviction: a sequence longer than C keeps its first n_sink and last n_recent tokens and the
@@ -64,10 +65,11 @@ def append(codes: np.ndarray, scales: np.ndarray, x: np.ndarray, scale_block: in
     """One token ``x [d]`` after ``codes [T, d]``, ``scales`` of its blocks (new arrays)."""
     T = codes.shape[0]
     need = block_scale(x, fmt)
+    amax = np.abs(x[np.isfinite(x)]).max(initial=0.0)
     codes, scales = codes.copy(), list(scales)
     if T % scale_block == 0:
         scales.append(need)
-    elif need > scales[-1]:
+    elif amax > QMAX[fmt] * scales[-1]:
         first = T // scale_block * scale_block
         codes[first:] = code_values(codes[first:] * (scales[-1] / need), fmt)
         scales[-1] = need

@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kAppendThreads) append8_kernel(KvView kv, cons
     if (bad) flag_status(ASP_DEV_NONFINITE);
     const int e = scale_exp<CT>(amax);
     const float need = exp2i(e);
-    const bool raise = in_block && need > was;
+    const bool raise = in_block && __uint_as_float(amax) > CT::kMax * was;   // the row does not fit
     // the codes: x / scale, exact for the powers of two the library writes
     float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll

@@ -35,6 +35,7 @@ struct CodeE4M3 {
   // which a value needs the next power of two, and the exponent it is taken off
   static constexpr uint32_t kTopFrac = 0x600000u;
   static constexpr int kShift = 9;
+  static constexpr float kMax = 448.f;
   // two codes (low, high byte) -> fp16x2 (low, high half), exact
   __device__ __forceinline__ static uint32_t pair(uint32_t w, int half) {
     uint32_t r;
@@ -65,6 +66,7 @@ struct CodeI8 {
   }
   static constexpr uint32_t kTopFrac = 0x7e0000u;   // 127 = 0.9921875 * 2^7
   static constexpr int kShift = 7;
+  static constexpr float kMax = 127.f;
   // The biased byte u = code + 128 below the fp16 pattern 0x6400 is 1024 + u; less 1152
   // it is the code, exact.
   __device__ __forceinline__ static uint32_t prep(uint32_t w) { return w ^ 0x80808080u; }
