@@ -174,9 +174,15 @@ class KV:
         self.k_scale, self.v_scale = k_scale, v_scale
         d = k.shape[-1]
         code = _CACHE_8.get(k.dtype)
+        self.is_8bit = code is not None
+        # types of an attention's output (an 8-bit cache: the query's) and of appended rows
+        self.out_dtype = None if self.is_8bit else k.dtype
+        self.row_dtype = src_dtype if self.is_8bit else k.dtype
         if code is None:
             code, k_scale, v_scale, scale_block = dtype_code(k), None, None, 0
         else:
+            if src_dtype not in (torch.float32, torch.bfloat16):
+                raise TypeError(f"src_dtype {src_dtype}: appended rows are float32 or bfloat16")
             if scale_block not in (16, 32, 64, 128):
                 raise ValueError(f"scale_block {scale_block}: 16, 32, 64 or 128 tokens share a scale")
             if v is not None and v.dtype != k.dtype:
@@ -207,6 +213,24 @@ class KV:
     @property
     def ref(self):
         return ctypes.byref(self.struct)
+
+    def check_out(self, fn: str, q: torch.Tensor, out: torch.Tensor) -> None:
+        want = self.out_dtype or q.dtype
+        if out.dtype != want:
+            raise TypeError(f"{fn}: out is {out.dtype}, this cache and a {q.dtype} query give {want}")
+
+    def check_rows(self, fn: str, k_new: torch.Tensor, v_new: torch.Tensor) -> None:
+        for x in (k_new, v_new):
+            if x is not None and x.dtype != self.row_dtype:
+                raise TypeError(f"{fn}: rows of {x.dtype}, this cache takes {self.row_dtype}")
+
+    def check_buffer(self, fn: str, name: str, x: torch.Tensor, dtype: torch.dtype, per_row: int) -> None:
+        """``x`` holds ``per_row`` values of every (sequence, KV head), contiguous."""
+        if x.dtype != dtype:
+            raise TypeError(f"{fn}: {name} is {x.dtype}, {dtype} is needed")
+        n = self.struct.batch * self.struct.n_kv_heads * per_row
+        if x.numel() < n or not x.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be contiguous and hold {n} values")
 
 
 class PredCfg:
@@ -274,6 +298,8 @@ def evict_workspace_bytes(kv: KV, C: int) -> int:
 def sparse_attend(q: torch.Tensor, kv: KV, idx: Optional[torch.Tensor], count: Optional[torch.Tensor], C: int,
                   out: torch.Tensor, lse: Optional[torch.Tensor] = None, tail_begin: Optional[torch.Tensor] = None,
                   max_tail: int = 0, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    if kv.is_8bit:
+        kv.check_out("sparse_attend", q, out)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check("asp_sparse_attend", lib().asp_sparse_attend(_ptr(q), dtype_code(q), q.shape[1], kv.ref, _ptr(idx),
                                                         _ptr(count), int(C), _ptr(tail_begin), int(max_tail),
@@ -297,6 +323,8 @@ def attend_accumulate(q: torch.Tensor, kv: KV, idx: Optional[torch.Tensor], coun
                       workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """:func:`sparse_attend` that also adds to ``acc [B, Hkv, t_max]`` (fp32) the softmax
     weight each attended token gets, summed over the query heads of its KV head."""
+    kv.check_out("attend_accumulate", q, out)
+    kv.check_buffer("attend_accumulate", "acc", acc, torch.float32, kv.t_max)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check("asp_attend_accumulate", lib().asp_attend_accumulate(
         _ptr(q), dtype_code(q), q.shape[1], kv.ref, _ptr(idx), _ptr(count), int(C), _ptr(tail_begin), int(max_tail),
@@ -310,6 +338,10 @@ def evict_kv(kv: KV, acc: torch.Tensor, C: int, idx: torch.Tensor, count: torch.
     and of the rest those with the largest ``acc``; they move to the front of the cache, in
     order, and ``kv.seq_lens`` shrinks on the device.  ``idx, count`` get the old positions,
     ``acc_out`` (``acc`` itself if None) the sums of the kept tokens."""
+    for name, x, dtype, per_row in (("acc", acc, torch.float32, kv.t_max), ("acc_out", acc_out, torch.float32, kv.t_max),
+                                    ("idx", idx, torch.int32, C), ("count", count, torch.int32, 1)):
+        if x is not None:
+            kv.check_buffer("evict_kv", name, x, dtype, per_row)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check("asp_evict_kv", lib().asp_evict_kv(kv.ref, _ptr(acc), _ptr(acc if acc_out is None else acc_out), int(C),
                                               int(n_sink), int(n_recent), _ptr(idx), _ptr(count), _ptr(workspace),
@@ -364,6 +396,8 @@ def append_kv(kv: KV, k_new: torch.Tensor, v_new: torch.Tensor, tail_begin: Opti
     """Appends one token per sequence (``k_new, v_new [B, Hkv, d]``) at position
     ``seq_lens[b]`` and advances ``kv.seq_lens`` on the device; ``tail_begin`` gets the
     old lengths; ``quest_meta`` (page bounds) is kept current."""
+    if kv.is_8bit:
+        kv.check_rows("append_kv", k_new, v_new)
     _check("asp_append_kv", lib().asp_append_kv(kv.ref, _ptr(k_new), _ptr(v_new), _ptr(tail_begin),
                                                 _ptr(quest_meta), int(quest_page), _stream(stream)))
 
@@ -494,6 +528,10 @@ class DecodeState:
              quest_meta: Optional[torch.Tensor] = None, quest_page: int = 16) -> None:
         """One decode step; with ``k_new``/``v_new`` the new token is appended first
         (``kv.seq_lens`` and ``tail_begin`` are then updated on the device)."""
+        if self.kv.is_8bit:
+            self.kv.check_out("step", q_t, out)
+            if k_new is not None:
+                self.kv.check_rows("step", k_new, v_new)
         a = self._args[self.cur]
         a.q_t = q_t.data_ptr()
         a.q_dtype = dtype_code(q_t)
