@@ -103,6 +103,8 @@ typedef enum { ASP_POOL_PREDICTIONS = 0, ASP_POOL_FEATURES = 1 } asp_pool_mode;
 #define ASP_DEV_NAN_SCORE  0x20  /* the selection read a NaN score: invalid input, the chosen set
                                     is then unspecified (it never holds more than C tokens) */
 #define ASP_DEV_NONFINITE  0x40  /* an infinity or NaN was written to an 8-bit cache (see asp_quantize_kv) */
+#define ASP_DEV_ROW_LIMIT  0x80  /* a sequence longer than the wide rows given was cut
+                                    (asp_quantize_kv_bounded, asp_dequantize_kv_bounded) */
 
 /* The KV cache of one layer.
  *   page_size == 0: k, v are [batch, n_kv_heads, t_max, head_dim] (contiguous).
@@ -346,7 +348,11 @@ ASP_API asp_status asp_append_kv(const asp_kv* kv, const void* k_new, const void
  * skipped and flagged (ASP_DEV_BAD_PAGE).
  * asp_dequantize_kv writes code * scale of the same tokens to k_dst, v_dst of dst_dtype
  * (laid out by strides in the same way), rounded to nearest; other tokens are not written.
- * Errors: ASP_ERR_INVALID_ARG (null, misaligned, bad types or negative strides);
+ * Both trust k_src .. v_dst to hold T_b tokens of every sequence.  The _bounded forms are for
+ * callers whose lengths live on the device: nothing past the first n_tokens >= 1 tokens of a
+ * sequence is read or written, and a longer sequence is cut to them and flagged
+ * (ASP_DEV_ROW_LIMIT).
+ * Errors: ASP_ERR_INVALID_ARG (null, misaligned, bad types, negative strides, n_tokens < 1);
  * ASP_ERR_UNSUPPORTED (a cache that is not 8-bit, head_dim not 64/128, scale_block not one
  * of 16, 32, 64, 128 or not dividing page_size). */
 ASP_API asp_status asp_quantize_kv(const asp_kv* kv, const void* k_src, const void* v_src, asp_dtype src_dtype,
@@ -355,6 +361,12 @@ ASP_API asp_status asp_quantize_kv(const asp_kv* kv, const void* k_src, const vo
 ASP_API asp_status asp_dequantize_kv(const asp_kv* kv, void* k_dst, void* v_dst, asp_dtype dst_dtype,
                                      int64_t stride_batch, int64_t stride_head, int64_t stride_token,
                                      asp_stream_t stream);
+ASP_API asp_status asp_quantize_kv_bounded(const asp_kv* kv, const void* k_src, const void* v_src,
+                                           asp_dtype src_dtype, int64_t n_tokens, int64_t stride_batch,
+                                           int64_t stride_head, int64_t stride_token, asp_stream_t stream);
+ASP_API asp_status asp_dequantize_kv_bounded(const asp_kv* kv, void* k_dst, void* v_dst, asp_dtype dst_dtype,
+                                             int64_t n_tokens, int64_t stride_batch, int64_t stride_head,
+                                             int64_t stride_token, asp_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Attention that also sums the weight each cached token gets (every cache type).

@@ -23,6 +23,7 @@ ASP_POOL_PREDICTIONS, ASP_POOL_FEATURES = 0, 1
 ASP_DEV_BAD_INDEX, ASP_DEV_BAD_PAGE, ASP_DEV_WAIT_LIMIT, ASP_DEV_TAIL_LIMIT, ASP_DEV_SELECT = 1, 2, 4, 8, 16
 ASP_DEV_NAN_SCORE = 32
 ASP_DEV_NONFINITE = 64
+ASP_DEV_ROW_LIMIT = 128
 
 # every entry point of include/asp.h with its ctypes signature
 class AspKv(ctypes.Structure):
@@ -68,6 +69,10 @@ SIGNATURES = {
     "asp_evict_workspace_bytes": (c_size_t, [POINTER(AspKv), c_int]),
     "asp_quantize_kv": (c_int, [POINTER(AspKv), c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p]),
     "asp_dequantize_kv": (c_int, [POINTER(AspKv), c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p]),
+    "asp_quantize_kv_bounded": (c_int, [POINTER(AspKv), c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64, c_int64,
+                                        c_void_p]),
+    "asp_dequantize_kv_bounded": (c_int, [POINTER(AspKv), c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64, c_int64,
+                                          c_void_p]),
     "asp_pred_factor_bytes": (c_size_t, [c_int, c_int, POINTER(AspPredCfg)]),
     "asp_sparse_attend_noalloc": (c_int, [c_void_p, c_int, c_int, POINTER(AspKv), c_void_p, c_void_p, c_int, c_void_p,
                                           c_int, c_void_p, c_void_p, c_void_p]),
@@ -356,20 +361,23 @@ def _rows8(fn: str, kv: KV, k: torch.Tensor, v: torch.Tensor):
                              f"contiguous channels")
     if k.dtype != v.dtype or k.stride() != v.stride():
         raise ValueError(f"{fn}: k and v must have the same type and strides")
-    return dtype_code(k), k.stride(0), k.stride(1), k.stride(2)
+    return dtype_code(k), min(k.shape[2], v.shape[2]), k.stride(0), k.stride(1), k.stride(2)
 
 
 def quantize_kv(kv: KV, k_src: torch.Tensor, v_src: torch.Tensor, stream=None) -> None:
     """Fills an 8-bit cache's tokens [0, seq_lens) from ``k_src, v_src [B, Hkv, tokens, d]``
-    (bf16 or fp32; any strides with contiguous channels, the same for both)."""
-    _check("asp_quantize_kv", lib().asp_quantize_kv(kv.ref, _ptr(k_src), _ptr(v_src),
-                                                    *_rows8("quantize_kv", kv, k_src, v_src), _stream(stream)))
+    (bf16 or fp32; any strides with contiguous channels, the same for both).  A sequence longer
+    than the rows is cut to them and flagged (``ASP_DEV_ROW_LIMIT``)."""
+    _check("asp_quantize_kv", lib().asp_quantize_kv_bounded(kv.ref, _ptr(k_src), _ptr(v_src),
+                                                            *_rows8("quantize_kv", kv, k_src, v_src), _stream(stream)))
 
 
 def dequantize_kv(kv: KV, k_dst: torch.Tensor, v_dst: torch.Tensor, stream=None) -> None:
-    """The values of an 8-bit cache's tokens [0, seq_lens) into ``k_dst, v_dst``."""
-    _check("asp_dequantize_kv", lib().asp_dequantize_kv(kv.ref, _ptr(k_dst), _ptr(v_dst),
-                                                        *_rows8("dequantize_kv", kv, k_dst, v_dst), _stream(stream)))
+    """The values of an 8-bit cache's tokens [0, seq_lens) into ``k_dst, v_dst`` (laid out and
+    bounded as in :func:`quantize_kv`)."""
+    _check("asp_dequantize_kv", lib().asp_dequantize_kv_bounded(kv.ref, _ptr(k_dst), _ptr(v_dst),
+                                                                *_rows8("dequantize_kv", kv, k_dst, v_dst),
+                                                                _stream(stream)))
 
 
 def quest_build_meta(kv: KV, quest_page: int, meta: torch.Tensor, stream=None) -> None:

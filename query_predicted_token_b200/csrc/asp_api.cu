@@ -266,12 +266,12 @@ cudaError_t append(const asp_kv* kv, const void* k_new, const void* v_new, int32
   return asp::launch_append(view_of(kv), k_new, v_new, lens, tail_begin, meta, quest_page, s);
 }
 
-asp_status check_rows8(const asp_kv* kv, const void* k, const void* v, asp_dtype dtype, int64_t sb, int64_t sh,
-                       int64_t st) {
+asp_status check_rows8(const asp_kv* kv, const void* k, const void* v, asp_dtype dtype, int64_t n_tokens, int64_t sb,
+                       int64_t sh, int64_t st) {
   const asp_status e = check_kv(kv, true, true);
   if (e != ASP_OK) return e;
   if (!is8(kv)) return ASP_ERR_UNSUPPORTED;
-  if (!k || !v || !aligned16(k) || !aligned16(v) || !is_wide(dtype)) return ASP_ERR_INVALID_ARG;
+  if (!k || !v || !aligned16(k) || !aligned16(v) || !is_wide(dtype) || n_tokens < 1) return ASP_ERR_INVALID_ARG;
   const int64_t per = dtype == ASP_F32 ? 4 : 8;   // elements of 16 bytes
   if (sb < 0 || sh < 0 || st < 0 || sb % per || sh % per || st % per) return ASP_ERR_INVALID_ARG;
   return ASP_OK;
@@ -483,22 +483,37 @@ asp_status asp_evict_kv(const asp_kv* kv, const float* acc, float* acc_out, int 
                                        reinterpret_cast<cudaStream_t>(stream)));
 }
 
-asp_status asp_quantize_kv(const asp_kv* kv, const void* k_src, const void* v_src, asp_dtype src_dtype,
-                           int64_t stride_batch, int64_t stride_head, int64_t stride_token, asp_stream_t stream) {
-  const asp_status st = check_rows8(kv, k_src, v_src, src_dtype, stride_batch, stride_head, stride_token);
+asp_status asp_quantize_kv_bounded(const asp_kv* kv, const void* k_src, const void* v_src, asp_dtype src_dtype,
+                                   int64_t n_tokens, int64_t stride_batch, int64_t stride_head, int64_t stride_token,
+                                   asp_stream_t stream) {
+  const asp_status st = check_rows8(kv, k_src, v_src, src_dtype, n_tokens, stride_batch, stride_head, stride_token);
   if (st != ASP_OK) return st;
   return cuda_status(asp::launch_quantize(view_of(kv), k_src, v_src, src_dtype == ASP_F32,
+                                          (int)(n_tokens < kv->t_max ? n_tokens : kv->t_max),
                                           asp::Strides3{stride_batch, stride_head, stride_token},
                                           reinterpret_cast<cudaStream_t>(stream)));
 }
 
-asp_status asp_dequantize_kv(const asp_kv* kv, void* k_dst, void* v_dst, asp_dtype dst_dtype, int64_t stride_batch,
-                             int64_t stride_head, int64_t stride_token, asp_stream_t stream) {
-  const asp_status st = check_rows8(kv, k_dst, v_dst, dst_dtype, stride_batch, stride_head, stride_token);
+asp_status asp_quantize_kv(const asp_kv* kv, const void* k_src, const void* v_src, asp_dtype src_dtype,
+                           int64_t stride_batch, int64_t stride_head, int64_t stride_token, asp_stream_t stream) {
+  return asp_quantize_kv_bounded(kv, k_src, v_src, src_dtype, INT64_MAX, stride_batch, stride_head, stride_token, stream);
+}
+
+asp_status asp_dequantize_kv_bounded(const asp_kv* kv, void* k_dst, void* v_dst, asp_dtype dst_dtype, int64_t n_tokens,
+                                     int64_t stride_batch, int64_t stride_head, int64_t stride_token,
+                                     asp_stream_t stream) {
+  const asp_status st = check_rows8(kv, k_dst, v_dst, dst_dtype, n_tokens, stride_batch, stride_head, stride_token);
   if (st != ASP_OK) return st;
   return cuda_status(asp::launch_dequantize(view_of(kv), k_dst, v_dst, dst_dtype == ASP_F32,
+                                            (int)(n_tokens < kv->t_max ? n_tokens : kv->t_max),
                                             asp::Strides3{stride_batch, stride_head, stride_token},
                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+asp_status asp_dequantize_kv(const asp_kv* kv, void* k_dst, void* v_dst, asp_dtype dst_dtype, int64_t stride_batch,
+                             int64_t stride_head, int64_t stride_token, asp_stream_t stream) {
+  return asp_dequantize_kv_bounded(kv, k_dst, v_dst, dst_dtype, INT64_MAX, stride_batch, stride_head, stride_token,
+                                   stream);
 }
 
 asp_status asp_decode_step(const asp_decode_args* a) {

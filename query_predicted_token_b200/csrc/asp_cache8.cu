@@ -11,6 +11,17 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Tokens of sequence b that the wide rows hold too; `flag`: this thread reports a longer one.
+__device__ __forceinline__ int bounded_len(const KvView& kv, long long b, int n_tokens, bool flag) {
+  int T = kv.seq_lens ? kv.seq_lens[b] : kv.t_max;
+  T = T > kv.t_max ? kv.t_max : T;
+  if (T > n_tokens) {
+    if (flag) flag_status(ASP_DEV_ROW_LIMIT);
+    T = n_tokens;
+  }
+  return T;
+}
+
 template <typename ST>
 struct Vec;   // 16 bytes of source values as fp32
 template <>
@@ -68,8 +79,8 @@ struct QuantLayout {
 
 template <typename ST, typename CT, int D, int BL>
 __global__ void __launch_bounds__(kThreads, QuantLayout<ST, CT, D, BL>::CTAS) quantize_kernel(KvView kv, const ST* __restrict__ k_src,
-                                                            const ST* __restrict__ v_src, Strides3 st, int nb,
-                                                            long long items) {
+                                                            const ST* __restrict__ v_src, Strides3 st, int n_tokens,
+                                                            int nb, long long items) {
   using L = QuantLayout<ST, CT, D, BL>;
   constexpr int N = L::N, VPR = L::VPR, NV = L::NV, TPB = L::TPB;
   __shared__ uint32_t wmax[2][kThreads / 32];
@@ -93,8 +104,7 @@ __global__ void __launch_bounds__(kThreads, QuantLayout<ST, CT, D, BL>::CTAS) qu
   auto load = [&](Block& q) {
     q.rows = 0;
     if (item < items) {
-      int T = kv.seq_lens ? kv.seq_lens[b] : kv.t_max;
-      T = T > kv.t_max ? kv.t_max : T;
+      const int T = bounded_len(kv, b, n_tokens, i == 0 && t == 0);
       const int tok0 = i * BL;
       q.rows = T - tok0 > BL ? BL : (T > tok0 ? T - tok0 : 0);
       if (q.rows) {
@@ -208,7 +218,8 @@ struct DeqLayout {
 
 template <typename DT, typename CT, int D, int UV>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(KvView kv, DT* __restrict__ k_dst,
-                                                              DT* __restrict__ v_dst, Strides3 st, int tiles) {
+                                                              DT* __restrict__ v_dst, Strides3 st, int n_tokens,
+                                                              int tiles) {
   using L = DeqLayout<DT, D, UV>;
   constexpr int N = L::N, VPR = L::VPR, U = L::U, ROWS = L::ROWS;
   const uint8_t* const code = static_cast<const uint8_t*>(blockIdx.z ? kv.v : kv.k);
@@ -218,8 +229,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(KvView kv, DT* __r
   const int unit = blockIdx.x;
   for (int tile = blockIdx.y; tile < tiles; tile += gridDim.y) {
     const int b = unit / kv.n_kv, h = unit - b * kv.n_kv;
-    int T = kv.seq_lens ? kv.seq_lens[b] : kv.t_max;
-    T = T > kv.t_max ? kv.t_max : T;
+    const int T = bounded_len(kv, b, n_tokens, tile == 0 && threadIdx.x == 0);
     if (tile * ROWS >= T) continue;
     uint32_t u[U][N / 4];
     float s[U];
@@ -367,9 +377,9 @@ __global__ void __launch_bounds__(kAppendThreads) append8_kernel(KvView kv, cons
 }
 
 template <typename ST, typename CT, int D, int BL>
-cudaError_t quantize_t(const KvView& kv, const void* k, const void* v, Strides3 st, cudaStream_t s) {
+cudaError_t quantize_t(const KvView& kv, const void* k, const void* v, int n, Strides3 st, cudaStream_t s) {
   constexpr int BPC = QuantLayout<ST, CT, D, BL>::BPC;
-  const int nb = (kv.t_max + BL - 1) / BL;
+  const int nb = (n + BL - 1) / BL;
   const long long items = (long long)kv.batch * nb * kv.n_kv;
   const long long ctas = (items + BPC - 1) / BPC;
   auto kern = quantize_kernel<ST, CT, D, BL>;
@@ -377,47 +387,48 @@ cudaError_t quantize_t(const KvView& kv, const void* k, const void* v, Strides3 
   if (per_sm < 1) return cudaErrorInvalidConfiguration;
   const long long most = ((long long)sm_count() * per_sm + 1) / 2;   // of each side
   kern<<<dim3((unsigned)(ctas < most ? ctas : most), 2), kThreads, 0, s>>>(kv, static_cast<const ST*>(k),
-                                                                           static_cast<const ST*>(v), st, nb, items);
+                                                                           static_cast<const ST*>(v), st, n, nb,
+                                                                           items);
   return cudaGetLastError();
 }
 
 template <typename ST, typename CT, int D>
-cudaError_t quantize_b(const KvView& kv, const void* k, const void* v, Strides3 st, cudaStream_t s) {
+cudaError_t quantize_b(const KvView& kv, const void* k, const void* v, int n, Strides3 st, cudaStream_t s) {
   switch (kv.block_shift) {
-    case 4: return quantize_t<ST, CT, D, 16>(kv, k, v, st, s);
-    case 5: return quantize_t<ST, CT, D, 32>(kv, k, v, st, s);
-    case 6: return quantize_t<ST, CT, D, 64>(kv, k, v, st, s);
-    case 7: return quantize_t<ST, CT, D, 128>(kv, k, v, st, s);
+    case 4: return quantize_t<ST, CT, D, 16>(kv, k, v, n, st, s);
+    case 5: return quantize_t<ST, CT, D, 32>(kv, k, v, n, st, s);
+    case 6: return quantize_t<ST, CT, D, 64>(kv, k, v, n, st, s);
+    case 7: return quantize_t<ST, CT, D, 128>(kv, k, v, n, st, s);
     default: return cudaErrorInvalidValue;
   }
 }
 
 template <typename ST, typename CT>
-cudaError_t quantize_d(const KvView& kv, const void* k, const void* v, Strides3 st, cudaStream_t s) {
-  return kv.head_dim == 64 ? quantize_b<ST, CT, 64>(kv, k, v, st, s) : quantize_b<ST, CT, 128>(kv, k, v, st, s);
+cudaError_t quantize_d(const KvView& kv, const void* k, const void* v, int n, Strides3 st, cudaStream_t s) {
+  return kv.head_dim == 64 ? quantize_b<ST, CT, 64>(kv, k, v, n, st, s) : quantize_b<ST, CT, 128>(kv, k, v, n, st, s);
 }
 
 template <typename DT, typename CT, int D, int UV>
-cudaError_t dequantize_u(const KvView& kv, void* k, void* v, Strides3 st, cudaStream_t s) {
+cudaError_t dequantize_u(const KvView& kv, void* k, void* v, int n, Strides3 st, cudaStream_t s) {
   constexpr int ROWS = DeqLayout<DT, D, UV>::ROWS;
-  const int tiles = (kv.t_max + ROWS - 1) / ROWS;
+  const int tiles = (n + ROWS - 1) / ROWS;
   dequantize_kernel<DT, CT, D, UV><<<dim3(kv.batch * kv.n_kv, tiles < 65535 ? tiles : 65535, 2), kThreads, 0, s>>>(
-      kv, static_cast<DT*>(k), static_cast<DT*>(v), st, tiles);
+      kv, static_cast<DT*>(k), static_cast<DT*>(v), st, n, tiles);
   return cudaGetLastError();
 }
 
 // Caches that would not fill the SMs with 8 vectors per thread take 2 (2 x 512 tokens, d = 64:
 // 2.9 against 4.4 us).
 template <typename DT, typename CT, int D>
-cudaError_t dequantize_t(const KvView& kv, void* k, void* v, Strides3 st, cudaStream_t s) {
+cudaError_t dequantize_t(const KvView& kv, void* k, void* v, int n, Strides3 st, cudaStream_t s) {
   constexpr int ROWS = DeqLayout<DT, D, 8>::ROWS;
-  const long long ctas = 2LL * kv.batch * kv.n_kv * ((kv.t_max + ROWS - 1) / ROWS);
-  return ctas < sm_count() ? dequantize_u<DT, CT, D, 2>(kv, k, v, st, s) : dequantize_u<DT, CT, D, 8>(kv, k, v, st, s);
+  const long long ctas = 2LL * kv.batch * kv.n_kv * ((n + ROWS - 1) / ROWS);
+  return ctas < sm_count() ? dequantize_u<DT, CT, D, 2>(kv, k, v, n, st, s) : dequantize_u<DT, CT, D, 8>(kv, k, v, n, st, s);
 }
 
 template <typename DT, typename CT>
-cudaError_t dequantize_d(const KvView& kv, void* k, void* v, Strides3 st, cudaStream_t s) {
-  return kv.head_dim == 64 ? dequantize_t<DT, CT, 64>(kv, k, v, st, s) : dequantize_t<DT, CT, 128>(kv, k, v, st, s);
+cudaError_t dequantize_d(const KvView& kv, void* k, void* v, int n, Strides3 st, cudaStream_t s) {
+  return kv.head_dim == 64 ? dequantize_t<DT, CT, 64>(kv, k, v, n, st, s) : dequantize_t<DT, CT, 128>(kv, k, v, n, st, s);
 }
 
 template <typename ST, typename CT>
@@ -433,21 +444,22 @@ cudaError_t append8_d(const KvView& kv, const void* k, const void* v, int32_t* l
 
 }  // namespace
 
-cudaError_t launch_quantize(const KvView& kv, const void* k_src, const void* v_src, int src_f32, Strides3 st,
-                            cudaStream_t s) {
+cudaError_t launch_quantize(const KvView& kv, const void* k_src, const void* v_src, int src_f32, int n_tokens,
+                            Strides3 st, cudaStream_t s) {
   if (kv.kv8 == 1)
-    return src_f32 ? quantize_d<float, CodeE4M3>(kv, k_src, v_src, st, s)
-                   : quantize_d<__nv_bfloat16, CodeE4M3>(kv, k_src, v_src, st, s);
-  return src_f32 ? quantize_d<float, CodeI8>(kv, k_src, v_src, st, s)
-                 : quantize_d<__nv_bfloat16, CodeI8>(kv, k_src, v_src, st, s);
+    return src_f32 ? quantize_d<float, CodeE4M3>(kv, k_src, v_src, n_tokens, st, s)
+                   : quantize_d<__nv_bfloat16, CodeE4M3>(kv, k_src, v_src, n_tokens, st, s);
+  return src_f32 ? quantize_d<float, CodeI8>(kv, k_src, v_src, n_tokens, st, s)
+                 : quantize_d<__nv_bfloat16, CodeI8>(kv, k_src, v_src, n_tokens, st, s);
 }
 
-cudaError_t launch_dequantize(const KvView& kv, void* k_dst, void* v_dst, int dst_f32, Strides3 st, cudaStream_t s) {
+cudaError_t launch_dequantize(const KvView& kv, void* k_dst, void* v_dst, int dst_f32, int n_tokens, Strides3 st,
+                              cudaStream_t s) {
   if (kv.kv8 == 1)
-    return dst_f32 ? dequantize_d<float, CodeE4M3>(kv, k_dst, v_dst, st, s)
-                   : dequantize_d<__nv_bfloat16, CodeE4M3>(kv, k_dst, v_dst, st, s);
-  return dst_f32 ? dequantize_d<float, CodeI8>(kv, k_dst, v_dst, st, s)
-                 : dequantize_d<__nv_bfloat16, CodeI8>(kv, k_dst, v_dst, st, s);
+    return dst_f32 ? dequantize_d<float, CodeE4M3>(kv, k_dst, v_dst, n_tokens, st, s)
+                   : dequantize_d<__nv_bfloat16, CodeE4M3>(kv, k_dst, v_dst, n_tokens, st, s);
+  return dst_f32 ? dequantize_d<float, CodeI8>(kv, k_dst, v_dst, n_tokens, st, s)
+                 : dequantize_d<__nv_bfloat16, CodeI8>(kv, k_dst, v_dst, n_tokens, st, s);
 }
 
 cudaError_t launch_append8(const KvView& kv, const void* k_new, const void* v_new, int src_f32, int32_t* seq_lens,

@@ -153,13 +153,15 @@ struct KvView {
 cudaError_t launch_append(const KvView& kv, const void* k_new, const void* v_new, int32_t* seq_lens,
                           int32_t* tail_begin, void* meta, int quest_page, cudaStream_t s);
 
-// 8-bit caches: the prompt's rows into codes and scales, and back.
+// 8-bit caches: the prompt's rows into codes and scales, and back; n_tokens: tokens of a
+// sequence that the wide rows hold, at most t_max.
 struct Strides3 {
   int64_t batch, head, token;   // elements
 };
-cudaError_t launch_quantize(const KvView& kv, const void* k_src, const void* v_src, int src_f32, Strides3 st,
+cudaError_t launch_quantize(const KvView& kv, const void* k_src, const void* v_src, int src_f32, int n_tokens, Strides3 st,
                             cudaStream_t s);
-cudaError_t launch_dequantize(const KvView& kv, void* k_dst, void* v_dst, int dst_f32, Strides3 st, cudaStream_t s);
+cudaError_t launch_dequantize(const KvView& kv, void* k_dst, void* v_dst, int dst_f32, int n_tokens, Strides3 st,
+                              cudaStream_t s);
 // The new token's rows (fp32 or bf16) into an 8-bit cache; as launch_append otherwise.
 cudaError_t launch_append8(const KvView& kv, const void* k_new, const void* v_new, int src_f32, int32_t* seq_lens,
                            int32_t* tail_begin, cudaStream_t s);

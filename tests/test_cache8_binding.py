@@ -96,3 +96,31 @@ def test_sums_are_fp32_of_every_token(fmt):
     for i, c in ((idx.long(), cnt), (idx[:, :, 1:].contiguous(), cnt), (idx, cnt.long()), (idx, cnt[:1])):
         with pytest.raises((TypeError, ValueError), match="idx|count"):
             asp.evict_kv(kv, good, C, i, c, stream=0)
+
+
+@pytest.mark.parametrize("call", ["quantize_kv", "dequantize_kv"])
+@pytest.mark.parametrize("nk,nv", [(40, 40), (64, 64), (80, 50), (17, 80)])
+def test_the_rows_token_count_bounds_the_call(monkeypatch, call, nk, nv):
+    """Lengths live on the device: the kernels must learn how many tokens the rows hold."""
+    seen = []
+
+    class Record:
+        def __getattr__(self, name):
+            return lambda *args: seen.append((name, args)) or L.ASP_OK
+
+    monkeypatch.setattr(L, "_lib", Record())
+    k = torch.zeros(B, H, 80, D)
+    getattr(asp, call)(cache8(), k[:, :, :nk], k[:, :, :nv], stream=0)
+    (name, args), = seen
+    assert name == f"asp_{call}_bounded"
+    assert args[3:8] == (L.ASP_F32, min(nk, nv), H * 80 * D, 80 * D, D)
+
+
+def test_the_bound_is_at_least_one_token(monkeypatch):
+    monkeypatch.setattr(L, "_lib", None)
+    from query_predicted_token_b200 import build
+    build.build()
+    kv = L.AspKv(2, 2, 128, 1024, L.ASP_I8, 0x10000, 0x10000, 0, None, 0, 0, 0x10000, 0x10000, 0x10000, 64, L.ASP_BF16)
+    for fn in (L.lib().asp_quantize_kv_bounded, L.lib().asp_dequantize_kv_bounded):
+        for n in (0, -1):
+            assert fn(kv, 0x10000, 0x10000, L.ASP_BF16, n, 1024, 512, 128, None) == L.ASP_ERR_INVALID_ARG
