@@ -379,8 +379,8 @@ ASP_API asp_status asp_dequantize_kv_bounded(const asp_kv* kv, void* k_dst, void
  * workspace  : asp_accumulate_workspace_bytes(...) bytes, 256-byte aligned, no
  *              initialisation needed; it holds the logits between the passes.  Two calls
  *              that may overlap (streams, captured graphs) need workspaces of their own.
- * Other arguments and errors as asp_sparse_attend; for an fp32 cache q must be 16-byte
- * aligned (ASP_ERR_INVALID_ARG). */
+ * Other arguments and errors as asp_sparse_attend; C + max_tail is at most 67 107 840
+ * (ASP_ERR_UNSUPPORTED); for an fp32 cache q must be 16-byte aligned (ASP_ERR_INVALID_ARG). */
 ASP_API asp_status asp_attend_accumulate(const void* q, asp_dtype q_dtype, int n_q_heads, const asp_kv* kv,
                                          const int32_t* idx, const int32_t* count, int C, const int32_t* tail_begin,
                                          int max_tail, void* out, float* lse, float* acc, void* workspace,

@@ -384,7 +384,7 @@ size_t asp_decode_workspace_bytes_kv(const asp_kv* kv, int n_q_heads, int C, int
 }
 
 size_t asp_accumulate_workspace_bytes(const asp_kv* kv, int n_q_heads, int C, int max_tail) {
-  if (!sizes_ok(kv, n_q_heads, C, max_tail)) return 0;
+  if (!sizes_ok(kv, n_q_heads, C, max_tail) || (long)C + max_tail > asp::kMaxAccumulateRows) return 0;
   if (kv->kv_dtype != ASP_F32) return flat_plan_of(kv, n_q_heads, C, max_tail, true, 0).workspace_bytes;
   return wide_accumulate(kv, n_q_heads, C, max_tail,
                          asp::attend_plan(kv->batch, n_q_heads, kv->n_kv_heads, kv->head_dim, C, max_tail).workspace_bytes)
@@ -443,6 +443,7 @@ asp_status asp_attend_accumulate(const void* q, asp_dtype q_dtype, int n_q_heads
   if (!acc) return ASP_ERR_INVALID_ARG;
   if (kv->kv_dtype == ASP_F32 && !aligned16(q)) return ASP_ERR_INVALID_ARG;   // read by whole vectors
   const int mt = tail_begin ? max_tail : 0;
+  if ((long)C + mt > asp::kMaxAccumulateRows) return ASP_ERR_UNSUPPORTED;
   const size_t need = asp_accumulate_workspace_bytes(kv, n_q_heads, C, mt);
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)) return ASP_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -197,6 +197,7 @@ constexpr size_t flat_smem(int G) {
 // The logits of rows r .. r + 3 (r a multiple of 4), one vector per head; rows past the unit's
 // and rows that were not attended hold -inf.
 constexpr int kAccRows = 4 * kFinThreads;   // of a CTA of finish_kernel
+static_assert(kMaxAccumulateRows == 65535L * kAccRows, "the sums' grid");
 
 struct RowLogits {
   float4 x[8];

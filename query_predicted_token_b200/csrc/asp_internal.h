@@ -256,6 +256,8 @@ struct FlatPlan {
   size_t part_off, info_off, logits_off;   // byte offsets in the workspace
   size_t workspace_bytes;
 };
+// Rows (C + max_tail) up to which the sums' launch has a grid: 65535 CTAs of 1024 rows per unit.
+constexpr long kMaxAccumulateRows = 65535L * 1024;
 // ctas_per_sm: 0 for a stand-alone call, 1 beside the key scan in the decode step.
 FlatPlan flat_plan(int batch, int n_q_heads, int n_kv_heads, int head_dim, int C, int max_tail, bool kv8,
                    bool accumulate, int ctas_per_sm);

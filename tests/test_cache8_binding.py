@@ -124,3 +124,19 @@ def test_the_bound_is_at_least_one_token(monkeypatch):
     for fn in (L.lib().asp_quantize_kv_bounded, L.lib().asp_dequantize_kv_bounded):
         for n in (0, -1):
             assert fn(kv, 0x10000, 0x10000, L.ASP_BF16, n, 1024, 512, 128, None) == L.ASP_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dtype", [L.ASP_F32, L.ASP_BF16, L.ASP_E4M3, L.ASP_I8])
+def test_rows_past_the_sums_grid_are_refused_before_the_attention_runs(monkeypatch, dtype):
+    """The sums' launch has 65535 CTAs of 1024 rows per unit at most."""
+    monkeypatch.setattr(L, "_lib", None)
+    from query_predicted_token_b200 import build
+    build.build()
+    lib, p = L.lib(), 0x10000
+    kv = L.AspKv(1, 1, 64, 1024, dtype, p, p, 0, None, 0, 0, p, p, p, 64, L.ASP_BF16)
+    most = 65535 * 1024
+    assert lib.asp_accumulate_workspace_bytes(kv, 1, 0, most) > 4 * most
+    for C, tail in ((0, most + 1), (1, most), (most, 1), (0, 1 << 30)):
+        assert lib.asp_accumulate_workspace_bytes(kv, 1, C, tail) == 0
+        st = lib.asp_attend_accumulate(p, L.ASP_BF16, 1, kv, p, p, C, p, tail, p, None, p, p, 1 << 60, None)
+        assert st == L.ASP_ERR_UNSUPPORTED
