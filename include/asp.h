@@ -352,7 +352,8 @@ ASP_API asp_status asp_append_kv(const asp_kv* kv, const void* k_new, const void
  * callers whose lengths live on the device: nothing past the first n_tokens >= 1 tokens of a
  * sequence is read or written, and a longer sequence is cut to them and flagged
  * (ASP_DEV_ROW_LIMIT).
- * Errors: ASP_ERR_INVALID_ARG (null, misaligned, bad types, negative strides, n_tokens < 1);
+ * Errors: ASP_ERR_INVALID_ARG (null, misaligned, bad types, negative strides, n_tokens < 1;
+ * destinations whose rows coincide: a stride of 0, tokens closer than head_dim);
  * ASP_ERR_UNSUPPORTED (a cache that is not 8-bit, head_dim not 64/128, scale_block not one
  * of 16, 32, 64, 128 or not dividing page_size). */
 ASP_API asp_status asp_quantize_kv(const asp_kv* kv, const void* k_src, const void* v_src, asp_dtype src_dtype,

@@ -500,11 +500,20 @@ asp_status asp_quantize_kv(const asp_kv* kv, const void* k_src, const void* v_sr
   return asp_quantize_kv_bounded(kv, k_src, v_src, src_dtype, INT64_MAX, stride_batch, stride_head, stride_token, stream);
 }
 
+namespace {
+// Rows of a destination lie apart: no stride of 0 over several sequences or heads, no token inside another.
+bool rows_apart(const asp_kv* kv, int64_t n_tokens, int64_t sb, int64_t sh, int64_t st) {
+  return (sb != 0 || kv->batch == 1) && (sh != 0 || kv->n_kv_heads == 1) &&
+         (st >= kv->head_dim || n_tokens == 1 || kv->t_max == 1);
+}
+}  // namespace
+
 asp_status asp_dequantize_kv_bounded(const asp_kv* kv, void* k_dst, void* v_dst, asp_dtype dst_dtype, int64_t n_tokens,
                                      int64_t stride_batch, int64_t stride_head, int64_t stride_token,
                                      asp_stream_t stream) {
   const asp_status st = check_rows8(kv, k_dst, v_dst, dst_dtype, n_tokens, stride_batch, stride_head, stride_token);
   if (st != ASP_OK) return st;
+  if (!rows_apart(kv, n_tokens, stride_batch, stride_head, stride_token)) return ASP_ERR_INVALID_ARG;
   return cuda_status(asp::launch_dequantize(view_of(kv), k_dst, v_dst, dst_dtype == ASP_F32,
                                             (int)(n_tokens < kv->t_max ? n_tokens : kv->t_max),
                                             asp::Strides3{stride_batch, stride_head, stride_token},

@@ -140,3 +140,16 @@ def test_rows_past_the_sums_grid_are_refused_before_the_attention_runs(monkeypat
         assert lib.asp_accumulate_workspace_bytes(kv, 1, C, tail) == 0
         st = lib.asp_attend_accumulate(p, L.ASP_BF16, 1, kv, p, p, C, p, tail, p, None, p, p, 1 << 60, None)
         assert st == L.ASP_ERR_UNSUPPORTED
+
+
+def test_rows_read_back_must_not_coincide(monkeypatch):
+    """A destination with a stride of 0, as expand() gives, would be written by many rows at once; a source may have one."""
+    monkeypatch.setattr(L, "_lib", None)
+    from query_predicted_token_b200 import build
+    build.build()
+    lib, p = L.lib(), 0x10000
+    for paged in (False, True):
+        kv = L.AspKv(2, 2, 128, 1024, L.ASP_I8, p, p, 64 if paged else 0, p, 16, 64, p, p, p, 64, L.ASP_BF16)
+        for st in ((0, 512, 128), (1024, 0, 128), (1024, 512, 0), (1024, 512, 64)):
+            assert lib.asp_dequantize_kv(kv, p, p, L.ASP_BF16, *st, None) == L.ASP_ERR_INVALID_ARG
+            assert lib.asp_dequantize_kv_bounded(kv, p, p, L.ASP_BF16, 8, *st, None) == L.ASP_ERR_INVALID_ARG
