@@ -500,11 +500,10 @@ __global__ void __launch_bounds__(kThreads, Fmt<CT>::kCtas) attend_flat_kernel(F
     float up = 1.f;
     if constexpr (F::kScaled) {   // largest channel to [2^14, 2^15)
       uint32_t amax = 0u;
-      bool bad = false;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
-        amax = max(max(amax, max(finite_abs(q4[ks].x, bad), finite_abs(q4[ks].y, bad))),
-                   max(finite_abs(q4[ks].z, bad), finite_abs(q4[ks].w, bad)));
+        amax = max(max(amax, max(finite_abs(q4[ks].x), finite_abs(q4[ks].y))),
+                   max(finite_abs(q4[ks].z), finite_abs(q4[ks].w)));
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       int e = (int)(amax >> 23) - 127;

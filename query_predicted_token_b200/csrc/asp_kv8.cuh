@@ -109,14 +109,14 @@ __device__ __forceinline__ int scale_exp(uint32_t amax_bits) {
 }
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126..127
 
-// |x| bits, 0 for an infinity or NaN (`bad` is then set)
-__device__ __forceinline__ uint32_t finite_abs(float x, bool& bad) {
+// |x| bits, 0 for an infinity or NaN (`bad` is then set, where given)
+__device__ __forceinline__ uint32_t finite_abs(float x) {
   const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
-  if (u >= 0x7f800000u) {
-    bad = true;
-    return 0u;
-  }
-  return u;
+  return u < 0x7f800000u ? u : 0u;
+}
+__device__ __forceinline__ uint32_t finite_abs(float x, bool& bad) {
+  bad |= (__float_as_uint(x) & 0x7fffffffu) >= 0x7f800000u;
+  return finite_abs(x);
 }
 
 }  // namespace asp

@@ -122,7 +122,7 @@ struct Query;
 
 template <int D, int NT>
 struct Query<CodeE4M3, D, NT> {   // NT = 1 for up to 4 heads, 2 for 8; column g of n-tile nt: part g & 1 of head 4 nt + g / 2
-  static constexpr int LD = D / 64;
+  static constexpr int LD = D / 64;     // 16-byte pieces of a row per lane
   uint32_t b[NT][4 * LD][2];
   float fac[NT];   // of head 4 nt + t: undoes the power of two, times 1 / sqrt(d)
 
@@ -133,13 +133,12 @@ struct Query<CodeE4M3, D, NT> {   // NT = 1 for up to 4 heads, 2 for 8; column g
       const bool has = head < p.G;
       const float* const src = p.qpred + ((size_t)bi * p.n_q_heads + h * p.G + (has ? head : 0)) * D + t * 16 * LD;
       uint32_t amax = 0u;
-      bool bad = false;
 #pragma unroll
       for (int i = 0; i < 4 * LD; ++i) {
         float x[4];
         ld_query(src + 4 * i, x);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) amax = max(amax, finite_abs(x[c], bad));
+        for (int c = 0; c < 4; ++c) amax = max(amax, finite_abs(x[c]));
       }
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
@@ -281,7 +280,6 @@ struct Ring {                          // of a warp
 template <typename CT, int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, 1) score8_kernel(Score8Params p) {
   using R = Ring<D>;
-  constexpr int LD = D / 64;           // 16-byte pieces of a row per lane
   const int S = p.stages;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int scratch[33];
@@ -350,7 +348,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) score8_kernel(Score8Params p) 
   // The window: the warp's next eight steps of unit (w_b, w_h), lane l holding the row (first
   // row of the tile in k; page checked) and the scale's place for tile l % 4 of step l / 4.  The
   // next one's page numbers are requested when a window opens.
-  int w_b = -1, w_h = -1, w_pos = 0, w_base = 0, n_page = 0;
+  int w_b = -1, w_h = -1, w_pos = 0, n_page = 0;
   uint32_t w_row = 0, w_srow = 0;
   constexpr int W_TILES = 8 * kWarps * kTiles;            // tiles from a window to the next
   const int l_tile = (lane / kTiles) * kWarps * kTiles + lane % kTiles;
@@ -384,7 +382,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) score8_kernel(Score8Params p) 
       const bool next = ic.b == w_b && ic.h == w_h;
       w_b = ic.b;
       w_h = ic.h;
-      w_base = t0;
       w_pos = 0;
       place(ic, t0 + l_tile, next ? n_page : page_at(ic, t0 + l_tile), w_row, w_srow);
       n_page = page_at(ic, t0 + W_TILES + l_tile);
