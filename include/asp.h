@@ -337,7 +337,9 @@ ASP_API asp_status asp_append_kv(const asp_kv* kv, const void* k_new, const void
  *   s = the smallest power of two >= 2^-100 with max |x| <= qmax * s   (qmax 448 or 127)
  * over the finite values of the block's tokens; a code is x / s (exact) rounded to the
  * nearest code, ties to even: for E4M3 an error of at most 2^-4 relative (half a step of
- * 3 fraction bits; 2^-10 s below 2^-6 s), for I8 at most s / 2.  Infinities become the
+ * 3 fraction bits; 2^-10 s below 2^-6 s), for I8 at most s / 2, that is max |x| / 127 at worst
+ * and max |x| / 254 at best (where a scale of max |x| / 127 would always give the latter: the
+ * power of two, which keeps every later change of scale exact, costs up to one bit).  Infinities become the
  * largest code, NaN the E4M3 NaN or the I8 zero, and either sets ASP_DEV_NONFINITE.
  *
  * asp_quantize_kv writes tokens [0, T_b) of every sequence from k_src, v_src (both

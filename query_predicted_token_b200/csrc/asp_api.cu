@@ -145,8 +145,8 @@ asp_status cuda_status(cudaError_t e) { return e == cudaSuccess ? ASP_OK : ASP_E
 
 // asp_decode_step's workspace: the attention's split-K partials, then (256-byte
 // aligned) the key-score histogram [batch * n_kv, 2048] int32 of the selection.
-// The decode step's attention runs beside the selection chain: one CTA per SM
-// leaves room for the key scan's CTA on every SM.
+// The decode step's attention runs beside the selection chain: one CTA per SM leaves room
+// for the key scan's CTA on every SM (8-bit caches: see flat_plan).
 constexpr int kDecodeAttendCtasPerSm = 1;
 
 size_t decode_hist_offset(int batch, int n_q_heads, int n_kv_heads, int head_dim, int C, int max_tail) {

@@ -26,7 +26,9 @@
 //    the exponents: they hold at any finite logit, whatever the spacing of floats there is.  m
 //    and R are integers, so rescaling is exact and no pair of scales leaves fp16's range.
 //    A weight keeps 11 bits (a second fp16 part, 22, for an fp32 query) down to 2^-28 of
-//    the largest.
+//    the largest.  A second part for a bf16 query as well would not show behind the output's own
+//    rounding to 8 bits (1.65e-3 against 1.64e-3 from the 64-bit result) and costs 6 to 14 %:
+//    8 x 32768 tokens 110.6 against 104.4 us, 2048 of each of 64 sequences 83.9 against 73.7.
 #include "asp_internal.h"
 #include "asp_kv8.cuh"
 
@@ -1053,9 +1055,15 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-// A unit of at most kWholeRows rows stays whole: four tiles per warp cost less than joining
-// the shares of several CTAs in a second launch (2 units of 512 rows, fp32 query: 11.2 us
-// shared).
+// A unit of at most kWholeRows rows stays whole: four tiles per warp cost no more than joining
+// the shares of several CTAs in a second launch, however few units there are.  E4M3, d = 128,
+// group 4, bf16 query, call times in us, whole against shared (the timer's step is 2 us):
+//   rows       1 to 8 units      128 units         512 units
+//    256       12.3 / 14 to 16   14.3 / 18.4       26.6 / 32.8
+//    512       16.4 / 16.4       16.4 / 24.6       32.8 / 36.9
+//    768       18.4 / 16.4       18.4 / 26.6       38.9 / 43.0
+//   2048       26 to 29 / 18     28.7 / 32.8       67.6 / 69.6
+// 512 is where whole units stop losing for few units; with an fp32 query or sums it is the same.
 constexpr int kWholeRows = 512;
 
 FlatPlan flat_plan(int batch, int n_q_heads, int n_kv_heads, int head_dim, int C, int max_tail, bool kv8,
@@ -1066,7 +1074,9 @@ FlatPlan flat_plan(int batch, int n_q_heads, int n_kv_heads, int head_dim, int C
   const int G = n_q_heads / n_kv_heads;
   const long tiles = units * ((rows + kTile - 1) / kTile);
   const long ctas = (tiles + kMinTiles - 1) / kMinTiles;
-  // the decode step leaves room beside the attention for the key scan: one CTA per SM
+  // beside the key scan in the decode step: one CTA per SM.  At d = 64 it shares the SM with a
+  // CTA of the scan; at d = 128 the two do not fit (286 KB of shared memory), and one is faster
+  // all the same: 94 us against 98 to 102 with two for a step at 8 x 32768, E4M3
   const long most = (long)kFlatSms * (ctas_per_sm > 0 ? ctas_per_sm : (kv8 ? Fmt<CodeE4M3>::kCtas : 1));
   pl.whole = rows <= kWholeRows ? 1 : 0;
   pl.ctas = (int)(pl.whole ? units : (ctas < most ? (ctas < 1 ? 1 : ctas) : most));

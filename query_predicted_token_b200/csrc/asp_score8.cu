@@ -6,12 +6,13 @@
 // The warps of a CTA take the 64-row steps of its contiguous range in turn.  Each has a ring of
 // three stages, filled by one bulk copy (TMA, 1-D) per 16-row tile, which never crosses a page,
 // counted on an mbarrier; page numbers come for eight steps at a time, one tile per lane, the
-// next eight ahead of their use.  The copies bound it: without any arithmetic the same copies
-// take 53 us of 54 (277 MB), and rings of 12 or 16 warps with the same bytes in flight 56 to 60.
+// next eight ahead of their use.  The copies bound it: a call over 269 MB takes 53 us with E4M3
+// codes and 57 with integers, and 53 with no arithmetic at all (rings of 12 or 16 warps with the
+// same bytes in flight: 56 to 60).
 // Lane (g, t) = (lane / 4, lane % 4) reads 16-byte pieces of rows g and g + 8 of a 16-row tile
 // from shared memory, which are its operand A; the order in which channels meet the k index
 // is the same for both operands and otherwise free.  (Rows loaded straight into registers, two
-// steps of them, spilled and waited: 52 us for 277 MB of E4M3, 112 us for 312 MB of integers.)
+// steps of them, spilled and waited: 112 us for 312 MB of integers.)
 // Every wait is bounded (ASP_DEV_WAIT_LIMIT).
 //
 // E4M3 codes are widened to fp16 (exact) for m16n8k16; the query, scaled by a power of two so
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) score8_kernel(Score8Params p) 
 
   const int total = pre[p.batch];
   // a CTA's steps follow one another and its warps take them in turn, so that it streams one
-  // region (a range per warp instead: 56 us for 277 MB even without any arithmetic)
+  // region (a range per warp instead: 56 us even without any arithmetic)
   const int i0 = (int)((long long)blockIdx.x * total / gridDim.x) + warp;
   const int i1 = (int)((long long)(blockIdx.x + 1) * total / gridDim.x);
   const int n = i1 > i0 ? (i1 - i0 + kWarps - 1) / kWarps : 0;
