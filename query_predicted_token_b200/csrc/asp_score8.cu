@@ -21,6 +21,8 @@
 // lie in memory, for m16n8k32 on integers: the query as a 23-bit integer of its largest
 // channel, in three 8-bit digits, one n-tile each.  Either way every product and every sum of
 // digits is exact; widening integer codes to fp16 instead takes 5 instructions per 4 codes.
+// The maximum over a group's heads keeps a NaN: a head that is not finite must not vanish behind
+// the others.
 #include <type_traits>
 
 #include "asp_internal.h"
@@ -83,14 +85,6 @@ __device__ __forceinline__ void mma_s8_0(int (&c)[4], uint32_t a0, uint32_t a1, 
       "{%10, %10, %10, %10};"
       : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
-}
-
-// Maximum that keeps a NaN (fmaxf drops it): a head that is not finite must not vanish behind its
-// group's others.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
 }
 
 // The query is read twice, for its largest channel and for its parts, so that only one piece of

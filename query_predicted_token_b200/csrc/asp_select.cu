@@ -520,13 +520,6 @@ __device__ __forceinline__ float edge_above(uint32_t k, int shift) {
   return e < k ? __uint_as_float(0x7fc00000u) : key_edge(e);
 }
 
-// max that propagates NaN (one operand NaN gives NaN)
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // The digit (of width nb, bins taken two (or one) per thread, highest first) that
 // holds the krem-th largest counted key; on return krem is the count still needed
 // from that bin, and the result says whether the bin holds exactly that many.
